@@ -4,6 +4,7 @@
 
 #include <stdint.h>
 
+#include "api.cuh"
 #include "common.cuh"
 #include "producer.cuh"
 
@@ -47,20 +48,45 @@ thread_local LaunchProbe t_probe;
 // The CUDA error behind this thread's last PRISM_ERR_CUDA (cudaSuccess if none yet).
 thread_local cudaError_t t_last_cuda_error = cudaSuccess;
 
+}  // namespace
+
+namespace prism {
+
 prism_status cuda_status(cudaError_t err) {
     if (err == cudaSuccess) return PRISM_OK;
     t_last_cuda_error = err;
     return PRISM_ERR_CUDA;
 }
 
-// Records the probe's last event after a probed call's final launch and disarms the probe.
 void probe_finish(cudaStream_t s) {
-    prism::launch_probe_mark(s);
+    launch_probe_mark(s);
     t_probe = LaunchProbe{};
 }
 
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-bool width_ok(int d) { return d == 32 || d == 64 || d == 128; }
+int sm_count() {
+    static int sms[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+    if (sms[dev] == 0) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+            n = 148;
+        sms[dev] = n;
+    }
+    return sms[dev];
+}
+
+int debug_flags() { return g_debug_flags; }
+
+}  // namespace prism
+
+namespace {
+
+using prism::aligned16;
+using prism::cuda_status;
+using prism::probe_finish;
+using prism::sm_count;
+using prism::width_ok;
 
 // Shared checks of prism_scan_fwd and prism_step_decode.
 prism_status check_common(const prism_shape *s, const void *q, const void *k, const void *v,
@@ -119,19 +145,6 @@ constexpr int kForceSegments = 2, kNoSegments = 4, kDebugStall = 8, kDebugForceW
 
 // Number of segments G of the segmented inter-chunk scan (1 = one in-order pass per sequence).
 // It needs dk == dv (the identity pass) and T divisible by G with at least one chunk per segment.
-int sm_count() {
-    static int sms[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-    if (sms[dev] == 0) {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-            n = 148;
-        sms[dev] = n;
-    }
-    return sms[dev];
-}
-
 // Measured on B200: on the Gated-DeltaNet route (whose in-order pass is latency-bound per chunk),
 // cutting 16 sequence slices of 65536 tokens into 16 segments halves the time; on the fused rank-L
 // route (one CTA per SM) the tripled work of the segmented scan does not pay.  So segments are

@@ -1,0 +1,96 @@
+// decay.cuh -- the decay scan (linear attention with one fixed decay per head): arguments and
+// launchers shared by its kernels and its C entry points.
+//
+//   S_t = a_h S_{t-1} + v_t k_t^T,   o_t = S_t q_t
+//
+// Every output of the forward and of the backward pass is one "pass" over the tokens with three
+// operands x, y [T, d1] and z [T, d2] of a head and a carried state R [d2, d1]:
+//   o_i = sum_{j <= i} a^(i-j) (x_i . y_j) z_j + (decayed entry state) x_i
+// With n tokens in a chunk, entry state R and the exit state R':
+//   forward in time:   o_i = sum_{j<=i} a^(i-j) (x_i.y_j) z_j + a^(i+1) R x_i,
+//                      R' = a^n R + sum_j a^(n-1-j) z_j y_j^T
+//   backward in time:  o_i = sum_{j>=i} a^(j-i) (x_i.y_j) z_j + a^(n-1-i) R x_i,
+//                      R' = a^n R + sum_j a^(j+1) z_j y_j^T
+//   o  : (x, y, z) = (q, k, v),  forward,  R = S
+//   dq : (dO, v, k),             forward,  R = S^T
+//   dk : (v, dO, q),             backward, R = G^T      (G_t = a G_{t+1} + dO_t q_t^T)
+//   dv : (k, q, dO),             backward, R = G
+// so the backward pass runs on the forward's kernels.
+//
+// The tokens are cut into segments of whole chunks, so that few sequences still fill the GPU:
+//   1. the sum kernel: every segment's contribution F = sum_j a^(...) z_j y_j^T to the state,
+//   2. the carry kernel: the segments' entry states from the F (and the exit state),
+//   3. the pass kernel: every segment's outputs from its entry state.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace prism {
+
+// One operand [B, T, heads, d] with unit stride along d; head h of the scan reads head h / div.
+struct DecayTensor {
+    const void *p;
+    long long sb, st, sh;  // elements between batches, tokens, heads
+    int div;
+};
+
+struct DecayPass {
+    int B, H, T, d1, d2;
+    DecayTensor x, y, z;  // widths d1, d1, d2
+    void *o;              // dense [B, T, H, d2]: io type, or fp32 when o_f32
+    int o_f32;
+    const float *decay;
+    const int *lengths;   // or null: every sequence has T tokens
+    // entry state of (b, h, segment): null (zero) or fp32 matrices one after the other,
+    // R[n][m] at n * d1 + m, or at m * d2 + n when entry_t
+    const float *entry;
+    int entry_t;
+    float *F;             // sum kernel's output, [B, H, nseg] matrices [d2][d1]
+    int reverse;
+    int nseg, seg_tokens; // segments per sequence, tokens per segment (whole chunks)
+};
+
+// Valid tokens of sequence b.
+__device__ __forceinline__ int decay_len(const int *lengths, int b, int T) {
+    if (!lengths) return T;
+    const int n = lengths[b];
+    return n < 0 ? 0 : (n > T ? T : n);
+}
+
+// a^n for a whole n >= 0 (0^0 = 1), computed in 64 bits: with a near 1 and n in the thousands a
+// 32-bit log would lose the last digits of the power.
+__device__ __forceinline__ float decay_pow(float a, int n) {
+    if (n == 0) return 1.f;
+    if (a == 0.f) return 0.f;
+    return (float)exp2((double)n * log2((double)a));
+}
+
+constexpr int kDecayChunkSimt = 64;
+
+cudaError_t launch_decay_sum_simt(const DecayPass &p, bool io_f32, cudaStream_t s);
+cudaError_t launch_decay_pass_simt(const DecayPass &p, bool io_f32, cudaStream_t s);
+
+// Entry states of every segment from the segments' sums, in place of them, and the exit state.
+struct DecayCarry {
+    int BH, H, T, elems;      // elems = d1 * d2
+    int nseg, seg_tokens, reverse;
+    const float *decay;
+    const int *lengths;
+    const float *init;        // [BH][elems] or null (zero)
+    float *F;                 // [BH][nseg][elems]: sums in, entry states out
+    float *final_state;       // [BH][elems] or null
+};
+cudaError_t launch_decay_carry(const DecayCarry &c, cudaStream_t s);
+
+// out[b,t,g,:] = sum over the `div` heads of group g of part[b,t,g*div + i,:] (fp32 -> io).
+cudaError_t launch_decay_group_sum(const float *part, void *out, long long rows, int groups, int div, int d,
+                                   bool io_f32, cudaStream_t s);
+
+cudaError_t launch_decay_step(int B, int H, int dk, int dv, const DecayTensor &q, const DecayTensor &k,
+                              const DecayTensor &v, const float *decay, float *S, void *o, bool io_f32,
+                              cudaStream_t s);
+
+}  // namespace prism

@@ -1,0 +1,327 @@
+// decay_simt.cu -- the decay scan's kernels on CUDA cores, in fp32 throughout (decay.cuh has the
+// formulas): the segment sums, the pass over the tokens, the carry between segments and the sum of
+// shared heads' gradients.
+
+#include "decay.cuh"
+
+namespace prism {
+namespace {
+
+constexpr int CH = kDecayChunkSimt;  // tokens of a chunk
+constexpr int NT = 256;              // 16 x 16 threads
+
+// Tile rows [t0, t0 + CH) of one head into shared memory as fp32, zero beyond `len` tokens and beyond
+// the operand's own width d (tiles are D = 64 or 128 columns wide, rows D + 4 floats apart: 16-byte
+// aligned, and 16 rows read at one column fall into different banks).
+template <typename IO, int D>
+__device__ __forceinline__ void load_tile(float *dst, const DecayTensor &x, int b, int h, int t0, int len, int d) {
+    constexpr int V = 16 / sizeof(IO);  // elements of a 16-byte load (d is a multiple of 32)
+    const IO *src = (const IO *)x.p + b * x.sb + (long long)(h / x.div) * x.sh;
+    for (int e = threadIdx.x; e < CH * (D / V); e += NT) {
+        const int r = e / (D / V), c = (e % (D / V)) * V;
+        float f[V];
+        if (t0 + r < len && c < d) {
+            const uint4 raw = *reinterpret_cast<const uint4 *>(src + (long long)(t0 + r) * x.st + c);
+            const IO *v = reinterpret_cast<const IO *>(&raw);
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[i] = ld_io(v, i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+            *reinterpret_cast<float4 *>(dst + r * (D + 4) + c + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+    }
+}
+
+// acc[r][c] += sum_j w_j Y[j][m0 + r] Z[j][n0 + c]: a thread's tile of the state, m along y, n along z
+// (4 consecutive columns out of every 64).
+template <int D1, int D2>
+__device__ __forceinline__ void state_tile(const float *Y, const float *Z, const float *w, float (&acc)[D1 / 16][D2 / 16]) {
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    for (int j = 0; j < CH; ++j) {
+        const float wj = w[j];
+        float4 y[D1 / 64], z[D2 / 64];
+#pragma unroll
+        for (int i = 0; i < D1 / 64; ++i) {
+            y[i] = *reinterpret_cast<const float4 *>(Y + j * (D1 + 4) + 64 * i + 4 * ty);
+            y[i].x *= wj; y[i].y *= wj; y[i].z *= wj; y[i].w *= wj;
+        }
+#pragma unroll
+        for (int i = 0; i < D2 / 64; ++i) z[i] = *reinterpret_cast<const float4 *>(Z + j * (D2 + 4) + 64 * i + 4 * tx);
+        const float *yf = &y[0].x, *zf = &z[0].x;
+#pragma unroll
+        for (int r = 0; r < D1 / 16; ++r)
+#pragma unroll
+            for (int c = 0; c < D2 / 16; ++c) acc[r][c] = fmaf(yf[r], zf[c], acc[r][c]);
+    }
+}
+
+// Column of the register tile's index i along y or z.
+__device__ __forceinline__ int tile_col(int i, int t) { return 64 * (i >> 2) + 4 * t + (i & 3); }
+
+// Weight of token j of a chunk with n valid ones in the state that leaves the chunk.
+__device__ __forceinline__ int write_exponent(int j, int n, int reverse) { return reverse ? j + 1 : n - 1 - j; }
+
+// F[n][m] of one segment: the state that its tokens alone leave behind.
+template <typename IO, int D1, int D2>
+__global__ void __launch_bounds__(NT) decay_sum_simt_kernel(DecayPass p) {
+    extern __shared__ __align__(16) float sm[];
+    float *Y = sm, *Z = Y + CH * (D1 + 4), *pw = Z + CH * (D2 + 4), *w = pw + CH + 1;
+    const int seg = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const int len = decay_len(p.lengths, b, p.T);
+    const int s0 = seg * p.seg_tokens;
+    const int s1 = min(s0 + p.seg_tokens, len);
+    const float a = p.decay[h];
+    for (int i = threadIdx.x; i <= CH; i += NT) pw[i] = decay_pow(a, i);
+    float acc[D1 / 16][D2 / 16] = {};
+    const int nch = s1 > s0 ? (s1 - s0 + CH - 1) / CH : 0;
+    for (int cc = 0; cc < nch; ++cc) {
+        const int t0 = s0 + (p.reverse ? nch - 1 - cc : cc) * CH;
+        const int n = min(CH, s1 - t0);
+        __syncthreads();
+        load_tile<IO, D1>(Y, p.y, b, h, t0, len, p.d1);
+        load_tile<IO, D2>(Z, p.z, b, h, t0, len, p.d2);
+        for (int j = threadIdx.x; j < CH; j += NT) w[j] = j < n ? pw[write_exponent(j, n, p.reverse)] : 0.f;
+        const float an = pw[n];
+#pragma unroll
+        for (int r = 0; r < D1 / 16; ++r)
+#pragma unroll
+            for (int c = 0; c < D2 / 16; ++c) acc[r][c] *= an;
+        __syncthreads();
+        state_tile<D1, D2>(Y, Z, w, acc);
+    }
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    float *F = p.F + (((long long)b * p.H + h) * p.nseg + seg) * p.d1 * p.d2;
+#pragma unroll
+    for (int r = 0; r < D1 / 16; ++r) {
+        const int m = tile_col(r, ty);
+#pragma unroll
+        for (int c = 0; c < D2 / 16; ++c) {
+            const int n = tile_col(c, tx);
+            if (m < p.d1 && n < p.d2) F[n * p.d1 + m] = acc[r][c];
+        }
+    }
+}
+
+// One segment's outputs, chunk by chunk, the state in shared memory (R^T: rows along y, so that the
+// entry term X R^T reads like the P Z product).
+template <typename IO, int D1, int D2>
+__global__ void __launch_bounds__(NT) decay_pass_simt_kernel(DecayPass p) {
+    extern __shared__ __align__(16) float sm[];
+    constexpr int PP = CH + 4;
+    float *X = sm, *Y = X + CH * (D1 + 4), *Z = Y + CH * (D1 + 4), *R = Z + CH * (D2 + 4), *P = R + D1 * (D2 + 4),
+          *pw = P + CH * PP, *w = pw + CH + 1;
+    const int seg = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int len = decay_len(p.lengths, b, p.T);
+    const int s0 = seg * p.seg_tokens;
+    const int send = min(s0 + p.seg_tokens, p.T), s1 = min(send, len);
+    const float a = p.decay[h];
+    for (int i = threadIdx.x; i <= CH; i += NT) pw[i] = decay_pow(a, i);
+    const float *E = p.entry ? p.entry + (((long long)b * p.H + h) * p.nseg + seg) * p.d1 * p.d2 : nullptr;
+    for (int e = threadIdx.x; e < D1 * D2; e += NT) {
+        // m fastest where R's rows are along y (n * d1 + m), n fastest otherwise
+        const int m = p.entry_t ? e / D2 : e % D1, n = p.entry_t ? e % D2 : e / D1;
+        float x = 0.f;
+        if (E && m < p.d1 && n < p.d2) x = E[p.entry_t ? m * p.d2 + n : n * p.d1 + m];
+        R[m * (D2 + 4) + n] = x;
+    }
+    auto store = [&](int t, int n, float x) {
+        const long long at = (((long long)b * p.T + t) * p.H + h) * p.d2 + n;
+        if (p.o_f32) ((float *)p.o)[at] = x;
+        else st_io((IO *)p.o, at, x);
+    };
+    const int nch = s1 > s0 ? (s1 - s0 + CH - 1) / CH : 0;
+    for (int cc = 0; cc < nch; ++cc) {
+        const int t0 = s0 + (p.reverse ? nch - 1 - cc : cc) * CH;
+        const int n = min(CH, s1 - t0);
+        __syncthreads();
+        load_tile<IO, D1>(X, p.x, b, h, t0, len, p.d1);
+        load_tile<IO, D1>(Y, p.y, b, h, t0, len, p.d1);
+        load_tile<IO, D2>(Z, p.z, b, h, t0, len, p.d2);
+        for (int j = threadIdx.x; j < CH; j += NT) w[j] = j < n ? pw[write_exponent(j, n, p.reverse)] : 0.f;
+        __syncthreads();
+        // P[i][j] = a^|i-j| x_i . y_j on the causal side, rows i = ty + 16 r, columns j = tx + 16 c
+        {
+            float s[4][4] = {};
+            for (int d = 0; d < D1; d += 4) {
+                float4 xv[4], yv[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    xv[r] = *reinterpret_cast<const float4 *>(X + (ty + 16 * r) * (D1 + 4) + d);
+                    yv[r] = *reinterpret_cast<const float4 *>(Y + (tx + 16 * r) * (D1 + 4) + d);
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        s[r][c] = fmaf(xv[r].x, yv[c].x, fmaf(xv[r].y, yv[c].y, fmaf(xv[r].z, yv[c].z, fmaf(xv[r].w, yv[c].w, s[r][c]))));
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int i = ty + 16 * r, j = tx + 16 * c, gap = p.reverse ? j - i : i - j;
+                    P[i * PP + j] = gap >= 0 ? s[r][c] * pw[gap] : 0.f;
+                }
+        }
+        __syncthreads();
+        float o[4][D2 / 16] = {};
+        // entry term, then scaled by its row's decay, then the chunk's own
+        for (int d = 0; d < D1; d += 4) {
+            float4 xv[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) xv[r] = *reinterpret_cast<const float4 *>(X + (ty + 16 * r) * (D1 + 4) + d);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int c4 = 0; c4 < D2 / 64; ++c4) {
+                    const float4 z = *reinterpret_cast<const float4 *>(R + (d + k) * (D2 + 4) + 64 * c4 + 4 * tx);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float x = (&xv[r].x)[k];
+                        o[r][4 * c4] = fmaf(x, z.x, o[r][4 * c4]);
+                        o[r][4 * c4 + 1] = fmaf(x, z.y, o[r][4 * c4 + 1]);
+                        o[r][4 * c4 + 2] = fmaf(x, z.z, o[r][4 * c4 + 2]);
+                        o[r][4 * c4 + 3] = fmaf(x, z.w, o[r][4 * c4 + 3]);
+                    }
+                }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = ty + 16 * r;
+            const float f = i < n ? pw[p.reverse ? n - 1 - i : i + 1] : 0.f;
+#pragma unroll
+            for (int c = 0; c < D2 / 16; ++c) o[r][c] *= f;
+        }
+        for (int j = 0; j < CH; j += 4) {
+            float4 xv[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) xv[r] = *reinterpret_cast<const float4 *>(P + (ty + 16 * r) * PP + j);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int c4 = 0; c4 < D2 / 64; ++c4) {
+                    const float4 z = *reinterpret_cast<const float4 *>(Z + (j + k) * (D2 + 4) + 64 * c4 + 4 * tx);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float x = (&xv[r].x)[k];
+                        o[r][4 * c4] = fmaf(x, z.x, o[r][4 * c4]);
+                        o[r][4 * c4 + 1] = fmaf(x, z.y, o[r][4 * c4 + 1]);
+                        o[r][4 * c4 + 2] = fmaf(x, z.z, o[r][4 * c4 + 2]);
+                        o[r][4 * c4 + 3] = fmaf(x, z.w, o[r][4 * c4 + 3]);
+                    }
+                }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = ty + 16 * r;
+            if (i >= n) continue;
+#pragma unroll
+            for (int c = 0; c < D2 / 16; ++c) {
+                const int col = tile_col(c, tx);
+                if (col < p.d2) store(t0 + i, col, o[r][c]);
+            }
+        }
+        if (cc + 1 < nch) {
+            float acc[D1 / 16][D2 / 16] = {};
+            state_tile<D1, D2>(Y, Z, w, acc);
+            __syncthreads();  // every thread has read R for its outputs
+            const float an = pw[n];
+#pragma unroll
+            for (int r = 0; r < D1 / 16; ++r)
+#pragma unroll
+                for (int c = 0; c < D2 / 16; ++c) {
+                    float &x = R[tile_col(r, ty) * (D2 + 4) + tile_col(c, tx)];
+                    x = fmaf(an, x, acc[r][c]);
+                }
+        }
+    }
+    // rows behind the sequence's last token
+    const int z0 = max(s0, s1);
+    for (int e = threadIdx.x; e < (send - z0) * p.d2; e += NT) store(z0 + e / p.d2, e % p.d2, 0.f);
+}
+
+template <typename IO, int D1, int D2>
+cudaError_t launch_one(const DecayPass &p, bool sum, cudaStream_t s) {
+    const int tiles = CH * (D1 + 4) + CH * (D2 + 4) + CH + 1 + CH;
+    const int bytes = 4 * (sum ? tiles : tiles + CH * (D1 + 4) + D1 * (D2 + 4) + CH * (CH + 4));
+    auto kern = sum ? decay_sum_simt_kernel<IO, D1, D2> : decay_pass_simt_kernel<IO, D1, D2>;
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err != cudaSuccess) return err;
+    launch_probe_mark(s);
+    kern<<<dim3(p.nseg, p.H, p.B), NT, bytes, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename IO>
+cudaError_t launch_widths(const DecayPass &p, bool sum, cudaStream_t s) {
+    if (p.d1 <= 64) return p.d2 <= 64 ? launch_one<IO, 64, 64>(p, sum, s) : launch_one<IO, 64, 128>(p, sum, s);
+    return p.d2 <= 64 ? launch_one<IO, 128, 64>(p, sum, s) : launch_one<IO, 128, 128>(p, sum, s);
+}
+
+// One thread per state element walks the segments in order: entry states replace the sums.
+__global__ void decay_carry_kernel(DecayCarry c) {
+    const int bh = blockIdx.x, e = blockIdx.y * blockDim.x + threadIdx.x;
+    const float a = c.decay[bh % c.H];
+    const int len = decay_len(c.lengths, bh / c.H, c.T);
+    if (e >= c.elems) return;
+    const float full = decay_pow(a, c.seg_tokens);
+    float *F = c.F + (long long)bh * c.nseg * c.elems + e;
+    float s = c.init ? c.init[(long long)bh * c.elems + e] : 0.f;
+    for (int i = 0; i < c.nseg; ++i) {
+        const int seg = c.reverse ? c.nseg - 1 - i : i;
+        const int n = min(max(len - seg * c.seg_tokens, 0), c.seg_tokens);
+        const float f = F[(long long)seg * c.elems];
+        F[(long long)seg * c.elems] = s;
+        if (n > 0) s = fmaf(n == c.seg_tokens ? full : decay_pow(a, n), s, f);
+    }
+    if (c.final_state) c.final_state[(long long)bh * c.elems + e] = s;
+}
+
+template <typename IO>
+__global__ void decay_group_sum_kernel(const float *part, IO *out, long long total, int div, int d) {
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;  // over [rows * groups, d / 4]
+    if (i >= total) return;
+    const long long g = i / (d / 4);
+    const int c = (int)(i % (d / 4)) * 4;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < div; ++k) {
+        const float4 x = *reinterpret_cast<const float4 *>(part + (g * div + k) * d + c);
+        s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+    }
+    st_io(out, g * d + c, s.x);
+    st_io(out, g * d + c + 1, s.y);
+    st_io(out, g * d + c + 2, s.z);
+    st_io(out, g * d + c + 3, s.w);
+}
+
+}  // namespace
+
+cudaError_t launch_decay_sum_simt(const DecayPass &p, bool io_f32, cudaStream_t s) {
+    return io_f32 ? launch_widths<float>(p, true, s) : launch_widths<__nv_bfloat16>(p, true, s);
+}
+
+cudaError_t launch_decay_pass_simt(const DecayPass &p, bool io_f32, cudaStream_t s) {
+    return io_f32 ? launch_widths<float>(p, false, s) : launch_widths<__nv_bfloat16>(p, false, s);
+}
+
+cudaError_t launch_decay_carry(const DecayCarry &c, cudaStream_t s) {
+    launch_probe_mark(s);
+    decay_carry_kernel<<<dim3(c.BH, (c.elems + 255) / 256), 256, 0, s>>>(c);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_decay_group_sum(const float *part, void *out, long long rows, int groups, int div, int d,
+                                   bool io_f32, cudaStream_t s) {
+    const long long total = rows * groups * (d / 4);
+    const unsigned blocks = (unsigned)((total + 255) / 256);
+    launch_probe_mark(s);
+    if (io_f32) decay_group_sum_kernel<float><<<blocks, 256, 0, s>>>(part, (float *)out, total, div, d);
+    else decay_group_sum_kernel<__nv_bfloat16><<<blocks, 256, 0, s>>>(part, (__nv_bfloat16 *)out, total, div, d);
+    return cudaGetLastError();
+}
+
+}  // namespace prism

@@ -17,6 +17,7 @@ LIB_PATH = os.path.join(_PKG, "libprism.so")
 
 PRISM_OK, PRISM_ERR_INVALID_ARG, PRISM_ERR_UNSUPPORTED, PRISM_ERR_CUDA, PRISM_ERR_TIMEOUT = range(5)
 PRISM_BF16, PRISM_F32 = 0, 1
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}  # prism_activation
 
 # Every symbol that include/prism.h declares.
 EXPORTS = (
@@ -30,6 +31,15 @@ EXPORTS = (
     "prism_state_fold",
     "prism_step_decode",
     "prism_write_producer",
+    "prism_decay_scan_fwd_workspace_size",
+    "prism_decay_scan_fwd",
+    "prism_decay_scan_bwd_workspace_size",
+    "prism_decay_scan_bwd",
+    "prism_decay_step",
+    "prism_group_norm_fwd_workspace_size",
+    "prism_group_norm_fwd",
+    "prism_group_norm_bwd_workspace_size",
+    "prism_group_norm_bwd",
     "prism_query_device_status",
     "prism_status_string",
     "prism_last_cuda_error",
@@ -54,6 +64,18 @@ class PrismShape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("T", ctypes.c_int),
                 ("dk", ctypes.c_int), ("dv", ctypes.c_int), ("L", ctypes.c_int),
                 ("chunk", ctypes.c_int), ("io", ctypes.c_int)]
+
+
+class PrismDecayShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("T", ctypes.c_int), ("Hkv", ctypes.c_int),
+                ("dk", ctypes.c_int), ("dv", ctypes.c_int), ("io", ctypes.c_int),
+                ("q_stride", ctypes.c_longlong * 3), ("k_stride", ctypes.c_longlong * 3),
+                ("v_stride", ctypes.c_longlong * 3)]
+
+
+class PrismNormShape(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int), ("S", ctypes.c_int), ("C", ctypes.c_int), ("G", ctypes.c_int),
+                ("io", ctypes.c_int), ("act", ctypes.c_int), ("eps", ctypes.c_float)]
 
 
 _lib = None
@@ -90,6 +112,18 @@ def load_library():
     lib.prism_step_decode.restype = ci
     lib.prism_write_producer.argtypes = [shp] + [vp] * 8 + [vp]
     lib.prism_write_producer.restype = ci
+    dshp, nshp = ctypes.POINTER(PrismDecayShape), ctypes.POINTER(PrismNormShape)
+    for name, argtypes in (("prism_decay_scan_fwd_workspace_size", [dshp, ctypes.POINTER(sz)]),
+                           ("prism_decay_scan_fwd", [dshp] + [vp] * 8 + [vp, sz, vp]),
+                           ("prism_decay_scan_bwd_workspace_size", [dshp, ctypes.POINTER(sz)]),
+                           ("prism_decay_scan_bwd", [dshp] + [vp] * 12 + [vp, sz, vp]),
+                           ("prism_decay_step", [dshp] + [vp] * 6 + [vp]),
+                           ("prism_group_norm_fwd_workspace_size", [nshp, ctypes.POINTER(sz)]),
+                           ("prism_group_norm_fwd", [nshp] + [vp] * 7 + [vp, sz, vp]),
+                           ("prism_group_norm_bwd_workspace_size", [nshp, ctypes.POINTER(sz)]),
+                           ("prism_group_norm_bwd", [nshp] + [vp] * 11 + [vp, sz, vp])):
+        getattr(lib, name).argtypes = argtypes
+        getattr(lib, name).restype = ci
     lib.prism_query_device_status.argtypes = [vp, vp]
     lib.prism_query_device_status.restype = ci
     lib.prism_status_string.argtypes = [ci]
@@ -446,3 +480,225 @@ def prism_state_fold(S_in, E, f, S_out=None, stream=None):
     if rc != PRISM_OK:
         raise PrismError(rc, "prism_state_fold")
     return S_out
+
+
+def _scratch(size_fn, where, shape, device, workspace) -> torch.Tensor:
+    """The caller's workspace, or a new one from torch's allocator: it belongs to this call alone, so
+    calls on several streams, and captured graphs, never share one."""
+    if workspace is not None:
+        _check_tensor("workspace", workspace, torch.uint8, (workspace.numel(),), device)
+        return workspace
+    need = ctypes.c_size_t(0)
+    rc = _call(device, size_fn, ctypes.byref(shape), ctypes.byref(need))
+    if rc != PRISM_OK:
+        raise PrismError(rc, where)
+    return torch.empty(need.value, dtype=torch.uint8, device=device)
+
+
+def _launched_on(stream, device, *tensors) -> None:
+    """Tensors that a call allocated and that its kernels use on another stream than the current one:
+    their memory is not handed out again before that stream has passed the call."""
+    if stream is not None and stream != torch.cuda.current_stream(device):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _check_view(name, x, dtype, shape, device):
+    """A tensor whose last dimension is dense and whose other strides are the library's to follow."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor (libprism has no CPU path)")
+    if x.device != device:
+        raise ValueError(f"{name} is on {x.device}, q is on {device}")
+    if x.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(x.shape)}")
+    if x.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
+    unit = 16 // x.element_size()
+    for n, st in zip(x.shape[:-1], x.stride()[:-1]):
+        if n > 1 and (st <= 0 or st % unit):
+            raise ValueError(f"{name}: strides must be positive multiples of 16 bytes, got {x.stride()} elements")
+
+
+def _decay_inputs(q, k, v, decay):
+    """Checks shared by the decay scan's entry points; returns (shape, device, io dtype)."""
+    for name, x in (("q", q), ("k", k), ("v", v)):
+        if not isinstance(x, torch.Tensor) or not x.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor (libprism has no CPU path)")
+        if x.dim() != 4:
+            raise ValueError(f"{name} must have 4 dimensions [B, T, heads, width], got {tuple(x.shape)}")
+    dev, io = q.device, q.dtype
+    if io not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"q must be torch.bfloat16 or torch.float32, got {io}")
+    B, T, H, dk = q.shape
+    Hkv, dv = k.shape[2], v.shape[3]
+    if Hkv < 1 or H % Hkv:
+        raise ValueError(f"k has {Hkv} heads, which do not divide the {H} heads of q")
+    _check_view("q", q, io, (B, T, H, dk), dev)
+    _check_view("k", k, io, (B, T, Hkv, dk), dev)
+    _check_view("v", v, io, (B, T, Hkv, dv), dev)
+    _check_tensor("decay", decay, torch.float32, (H,), dev)
+    if decay is None:
+        raise TypeError("decay must be a CUDA tensor (libprism has no CPU path)")
+    strides = [(ctypes.c_longlong * 3)(*x.stride()[:3]) for x in (q, k, v)]
+    shape = PrismDecayShape(B, H, T, Hkv, dk, dv, PRISM_F32 if io == torch.float32 else PRISM_BF16, *strides)
+    return shape, dev, io
+
+
+def prism_decay_scan_fwd(q, k, v, decay, S0=None, lengths=None, *, o=None, S_final=None, want_state=True,
+                         workspace=None, stream=None):
+    """The decay scan (include/prism.h): S_t = decay_h S_{t-1} + v_t k_t^T, o_t = S_t q_t.  q: [B,T,H,dk];
+    k, v: [B,T,Hkv,dk], [B,T,Hkv,dv] with Hkv dividing H; q, k, v may be strided views (unit stride along
+    the width, other strides multiples of 16 bytes); decay: [H] fp32 in [0, 1]; S0: [B,H,dv,dk] fp32 or
+    None; lengths: [B] int32 (valid tokens of a padded batch) or None.  Returns (o [B,T,H,dv], S_final
+    [B,H,dv,dk] fp32 or None)."""
+    lib = load_library()
+    shape, dev, io = _decay_inputs(q, k, v, decay)
+    B, T, H, dk, dv = shape.B, shape.T, shape.H, shape.dk, shape.dv
+    f32 = torch.float32
+    _check_tensor("S0", S0, f32, (B, H, dv, dk), dev)
+    _check_tensor("lengths", lengths, torch.int32, (B,), dev)
+    if o is None:
+        o = torch.empty((B, T, H, dv), dtype=io, device=dev)
+    _check_tensor("o", o, io, (B, T, H, dv), dev)
+    if S_final is None and want_state:
+        S_final = torch.empty((B, H, dv, dk), dtype=f32, device=dev)
+    _check_tensor("S_final", S_final, f32, (B, H, dv, dk), dev)
+    ws = _scratch(lib.prism_decay_scan_fwd_workspace_size, "prism_decay_scan_fwd_workspace_size", shape, dev, workspace)
+    rc = _call(dev, lib.prism_decay_scan_fwd, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(S0),
+               _ptr(lengths), _ptr(o), _ptr(S_final), _ptr(ws), ctypes.c_size_t(ws.numel()), _stream(stream, dev))
+    if rc != PRISM_OK:
+        raise PrismError(rc, "prism_decay_scan_fwd")
+    _launched_on(stream, dev, o, S_final, ws)
+    return o, S_final
+
+
+def prism_decay_scan_bwd(q, k, v, decay, S0=None, lengths=None, *, dO, dS_final=None, want_dS0=True,
+                         workspace=None, stream=None):
+    """Backward of prism_decay_scan_fwd.  Inputs as there; dO: [B,T,H,dv] (io dtype, dense); dS_final:
+    [B,H,dv,dk] fp32 or None.  Returns a dict with dq [B,T,H,dk], dk [B,T,Hkv,dk], dv [B,T,Hkv,dv] in
+    the inputs' type and dS0 [B,H,dv,dk] fp32 (or None)."""
+    lib = load_library()
+    shape, dev, io = _decay_inputs(q, k, v, decay)
+    B, T, H, dk, dv = shape.B, shape.T, shape.H, shape.dk, shape.dv
+    f32 = torch.float32
+    _check_tensor("S0", S0, f32, (B, H, dv, dk), dev)
+    _check_tensor("lengths", lengths, torch.int32, (B,), dev)
+    if dO is None:
+        raise TypeError("dO must be a CUDA tensor (libprism has no CPU path)")
+    _check_tensor("dO", dO, io, (B, T, H, dv), dev)
+    _check_tensor("dS_final", dS_final, f32, (B, H, dv, dk), dev)
+    out = {"dq": torch.empty((B, T, H, dk), dtype=io, device=dev),
+           "dk": torch.empty((B, T, shape.Hkv, dk), dtype=io, device=dev),
+           "dv": torch.empty((B, T, shape.Hkv, dv), dtype=io, device=dev),
+           "dS0": torch.empty((B, H, dv, dk), dtype=f32, device=dev) if want_dS0 else None}
+    ws = _scratch(lib.prism_decay_scan_bwd_workspace_size, "prism_decay_scan_bwd_workspace_size", shape, dev, workspace)
+    rc = _call(dev, lib.prism_decay_scan_bwd, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(S0),
+               _ptr(lengths), _ptr(dO), _ptr(dS_final), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
+               _ptr(out["dS0"]), _ptr(ws), ctypes.c_size_t(ws.numel()), _stream(stream, dev))
+    if rc != PRISM_OK:
+        raise PrismError(rc, "prism_decay_scan_bwd")
+    _launched_on(stream, dev, ws, *out.values())
+    return out
+
+
+def prism_decay_step(q, k, v, decay, S, *, o=None, stream=None):
+    """One token of the decay scan, S [B,H,dv,dk] fp32 updated in place.  q: [B,1,H,dk]; k, v: [B,1,Hkv,dk],
+    [B,1,Hkv,dv] (views as for prism_decay_scan_fwd); decay: [H] fp32.  Returns o [B,1,H,dv]."""
+    lib = load_library()
+    shape, dev, io = _decay_inputs(q, k, v, decay)
+    B, T, H, dk, dv = shape.B, shape.T, shape.H, shape.dk, shape.dv
+    if S is None:
+        raise TypeError("S must be a CUDA tensor (libprism has no CPU path)")
+    _check_tensor("S", S, torch.float32, (B, H, dv, dk), dev)
+    if o is None:
+        o = torch.empty((B, T, H, dv), dtype=io, device=dev)
+    _check_tensor("o", o, io, (B, T, H, dv), dev)
+    rc = _call(dev, lib.prism_decay_step, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(S),
+               _ptr(o), _stream(stream, dev))
+    if rc != PRISM_OK:
+        raise PrismError(rc, "prism_decay_step")
+    _launched_on(stream, dev, o)
+    return o
+
+
+def _norm_inputs(x, groups, weight, bias, gate, eps, activation):
+    """Checks shared by the group norm's entry points; returns (shape, device, io dtype)."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError("x must be a CUDA tensor (libprism has no CPU path)")
+    if x.dim() < 2:
+        raise ValueError(f"x must have at least 2 dimensions [N, ..., C], got {tuple(x.shape)}")
+    dev, io = x.device, x.dtype
+    if io not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {io}")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
+    N, C = x.shape[0], x.shape[-1]
+    S = 1
+    for n in x.shape[1:-1]:
+        S *= n
+    if groups < 1 or C < 1 or C % groups:
+        raise ValueError(f"{groups} groups do not divide {C} channels")
+    if S > 0x7FFFFFFF:
+        raise ValueError(f"x has {S} positions, the library takes up to 2^31 - 1")
+    _check_tensor("x", x, io, x.shape, dev)
+    _check_tensor("weight", weight, torch.float32, (C,), dev)
+    _check_tensor("bias", bias, torch.float32, (C,), dev)
+    _check_tensor("gate", gate, io, x.shape, dev)
+    shape = PrismNormShape(N, S, C, groups, PRISM_F32 if io == torch.float32 else PRISM_BF16, ACTIVATIONS[activation], eps)
+    return shape, dev, io
+
+
+def prism_group_norm_fwd(x, groups, weight=None, bias=None, gate=None, *, eps=1e-5, activation="none", y=None,
+                         workspace=None, stream=None):
+    """Group norm with an activation, channels last (include/prism.h).  x: [N, ..., C] (statistics over the
+    middle dimensions and each group's C / groups channels; [tokens, C] normalises every token on its
+    own); weight, bias: [C] fp32 or None; gate: like x or None; activation: "none", "silu" or "gelu", of
+    the result, or of the gate that multiplies it.  Returns (y, mean, rstd), the last two [N, groups]
+    fp32 for prism_group_norm_bwd."""
+    lib = load_library()
+    shape, dev, io = _norm_inputs(x, groups, weight, bias, gate, eps, activation)
+    if y is None:
+        y = torch.empty_like(x)
+    _check_tensor("y", y, io, x.shape, dev)
+    mean = torch.empty((shape.N, groups), dtype=torch.float32, device=dev)
+    rstd = torch.empty_like(mean)
+    ws = _scratch(lib.prism_group_norm_fwd_workspace_size, "prism_group_norm_fwd_workspace_size", shape, dev, workspace)
+    rc = _call(dev, lib.prism_group_norm_fwd, ctypes.byref(shape), _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate),
+               _ptr(y), _ptr(mean), _ptr(rstd), _ptr(ws), ctypes.c_size_t(ws.numel()), _stream(stream, dev))
+    if rc != PRISM_OK:
+        raise PrismError(rc, "prism_group_norm_fwd")
+    _launched_on(stream, dev, y, mean, rstd, ws)
+    return y, mean, rstd
+
+
+def prism_group_norm_bwd(x, groups, mean, rstd, weight=None, bias=None, gate=None, *, dy, activation="none",
+                         workspace=None, stream=None):
+    """Backward of prism_group_norm_fwd: its inputs, the mean and rstd it returned, and dy like x.  Returns
+    a dict with dx, and dgate, dweight, dbias where gate, weight, bias are given."""
+    lib = load_library()
+    shape, dev, io = _norm_inputs(x, groups, weight, bias, gate, 0.0, activation)
+    for name, t in (("mean", mean), ("rstd", rstd), ("dy", dy)):
+        if t is None:
+            raise TypeError(f"{name} must be a CUDA tensor (libprism has no CPU path)")
+    f32 = torch.float32
+    _check_tensor("mean", mean, f32, (shape.N, groups), dev)
+    _check_tensor("rstd", rstd, f32, (shape.N, groups), dev)
+    _check_tensor("dy", dy, io, x.shape, dev)
+    out = {"dx": torch.empty_like(x)}
+    if gate is not None:
+        out["dgate"] = torch.empty_like(x)
+    if weight is not None:
+        out["dweight"] = torch.empty_like(weight)
+    if bias is not None:
+        out["dbias"] = torch.empty_like(bias)
+    ws = _scratch(lib.prism_group_norm_bwd_workspace_size, "prism_group_norm_bwd_workspace_size", shape, dev, workspace)
+    rc = _call(dev, lib.prism_group_norm_bwd, ctypes.byref(shape), _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate),
+               _ptr(mean), _ptr(rstd), _ptr(dy), _ptr(out["dx"]), _ptr(out.get("dgate")), _ptr(out.get("dweight")),
+               _ptr(out.get("dbias")), _ptr(ws), ctypes.c_size_t(ws.numel()), _stream(stream, dev))
+    if rc != PRISM_OK:
+        raise PrismError(rc, "prism_group_norm_bwd")
+    _launched_on(stream, dev, ws, *out.values())
+    return out

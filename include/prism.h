@@ -241,6 +241,155 @@ prism_status prism_write_producer(const prism_shape *shape, const void *x, const
                                   const float *beta, void *u, void *w, void *stream);
 
 /*
+ * The decay scan: linear attention with one fixed decay per head, the write without an erase term
+ * (prism_scan_fwd with beta = 0, u = v, w = k and alpha_t = decay[h] for every t):
+ *
+ *     S_t = decay_h S_{t-1} + v_t k_t^T,     o_t = S_t q_t
+ *
+ * For a prompt (prism_decay_scan_fwd), its gradients (prism_decay_scan_bwd) and single tokens
+ * (prism_decay_step).  The affine elements of "Sequential Parallel Duality in Prefix Scannable
+ * Models" (key design 2) have E_t = decay I here, so a chunk needs no triangular solve and the
+ * sequence is cut into segments whose states combine by a scalar power.
+ */
+typedef struct {
+    int B, H, T;      /* batch, query heads, tokens (T >= 0; prism_decay_step requires T == 1)    */
+    int Hkv;          /* key / value heads, a divisor of H: query head h reads head h / (H / Hkv) */
+    int dk, dv;       /* key and value widths, each in {32, 64, 128}                              */
+    prism_dtype io;   /* type of q, k, v, o and of their gradients (decay and states are fp32)    */
+    /* Elements between consecutive batches, tokens and heads of q, k and v (unit stride along the
+     * width), so that views of a fused projection need no copy.  All three zero: dense.  Strides
+     * along an extent of 0 or 1 are ignored; the others are positive multiples of 16 bytes.       */
+    long long q_stride[3], k_stride[3], v_stride[3];
+} prism_decay_shape;
+
+/* prism_decay_scan_fwd_workspace_size -- bytes of device workspace prism_decay_scan_fwd needs for
+ * `shape` (the segments' states).  Depends on the current device's SM count.  Writes *bytes. */
+prism_status prism_decay_scan_fwd_workspace_size(const prism_decay_shape *shape, size_t *bytes);
+
+/*
+ * prism_decay_scan_fwd -- the decay scan over T tokens of all B*H sequences.
+ *   q        [B,T,H,dk] io, k [B,T,Hkv,dk] io, v [B,T,Hkv,dv] io   (strides as in `shape`)
+ *   decay    [H] fp32              in [0, 1] (0: only the token itself)
+ *   S0       [B,H,dv,dk] fp32      entry state, or NULL for zeros
+ *   lengths  [B] int32             valid tokens of each sequence of a padded batch (clamped to
+ *                                  [0, T]), or NULL: every sequence has T.  Tokens behind a
+ *                                  sequence's end may hold anything, NaN included: they enter no
+ *                                  state, and their rows of o are zero.
+ *   o        [B,T,H,dv] io         output, dense
+ *   S_final  [B,H,dv,dk] fp32      state after each sequence's last token, or NULL to skip;
+ *                                  S_final == S0 is allowed
+ *   workspace, ws_bytes            at least prism_decay_scan_fwd_workspace_size bytes, 256-byte
+ *                                  aligned; needs no clearing, and nothing in it outlives the call
+ * No other overlap of an output with an input or output is allowed.  B, H <= 65535 and B*H <= 2^24.
+ * States and sums are fp32.  bf16 outputs are rounded to nearest even; inside, the products of a
+ * chunk and the state are rounded to bf16 once where they enter an output's product, never where
+ * they enter a state.  A non-finite value in a valid token reaches outputs of its whole 128-token
+ * chunk and of every later token.  Results do not depend on the run (no atomics).
+ */
+prism_status prism_decay_scan_fwd(const prism_decay_shape *shape, const void *q, const void *k,
+                                  const void *v, const float *decay, const float *S0,
+                                  const int *lengths, void *o, float *S_final, void *workspace,
+                                  size_t ws_bytes, void *stream);
+
+/* prism_decay_scan_bwd_workspace_size -- bytes of device workspace prism_decay_scan_bwd needs for
+ * `shape` (the segments' states and state gradients; with Hkv < H also fp32 gradients of one shared
+ * operand per query head).  Depends on the current device's SM count.  Writes *bytes. */
+prism_status prism_decay_scan_bwd_workspace_size(const prism_decay_shape *shape, size_t *bytes);
+
+/*
+ * prism_decay_scan_bwd -- gradients of prism_decay_scan_fwd's q, k, v and S0.  With G_t the gradient of
+ * S_t (running from dS_final at the last token to the first):
+ *   G_t += dO_t q_t^T;   dq_t = S_t^T dO_t;   dk_t = G_t^T v_t;   dv_t = G_t k_t;
+ *   G_{t-1} = decay_h G_t;   dS0 = G_0;   dk, dv of a shared head: the sum over its query heads.
+ * The decay is a constant of the head and gets no gradient (prism_scan_bwd gives the gradient of a
+ * decay per token).
+ *   q, k, v, decay, S0, lengths   as passed to prism_decay_scan_fwd
+ *   dO        [B,T,H,dv] io        upstream gradient of o, dense (rows behind a sequence's end are
+ *                                  not used)
+ *   dS_final  [B,H,dv,dk] fp32     upstream gradient of S_final, or NULL for zero
+ *   dq        [B,T,H,dk] io, dk [B,T,Hkv,dk] io, dv [B,T,Hkv,dv] io   outputs, dense, in the
+ *                                  inputs' type; zero behind a sequence's end
+ *   dS0       [B,H,dv,dk] fp32     output, or NULL to skip
+ *   workspace, ws_bytes            at least prism_decay_scan_bwd_workspace_size bytes, 256-byte
+ *                                  aligned; needs no clearing
+ * No output may overlap an input or another output.  Rounding as for prism_decay_scan_fwd.
+ */
+prism_status prism_decay_scan_bwd(const prism_decay_shape *shape, const void *q, const void *k,
+                                  const void *v, const float *decay, const float *S0,
+                                  const int *lengths, const void *dO, const float *dS_final,
+                                  void *dq, void *dk, void *dv, float *dS0, void *workspace,
+                                  size_t ws_bytes, void *stream);
+
+/*
+ * prism_decay_step -- one token for each of the B*H sequences (shape->T must be 1):
+ *   S <- decay_h S + v k^T   (in place, [B,H,dv,dk] fp32),   o = S q   ([B,1,H,dv] io).
+ * q, k, v and decay as for prism_decay_scan_fwd.  One read and one write of S, in fp32.
+ */
+prism_status prism_decay_step(const prism_decay_shape *shape, const void *q, const void *k,
+                              const void *v, const float *decay, float *S, void *o, void *stream);
+
+/*
+ * Group norm with an activation, channels last: the norm behind a scan (one group per head, every
+ * token on its own) and over positions.  x [N, S, C] with G groups of C / G neighbouring channels;
+ * the statistics of (sample n, group g) go over its S positions and C / G channels:
+ *
+ *     z = (x - mean) rstd weight_c + bias_c,   rstd = 1 / sqrt(var + eps)   (var without Bessel's
+ *     y = act(z)   or, with a gate,   y = z act(gate)                        correction)
+ *
+ * For the outputs o [B,T,H,dv] of a scan: N = B T, S = 1, C = H dv, G = H.
+ */
+typedef enum { PRISM_ACT_NONE = 0, PRISM_ACT_SILU = 1, PRISM_ACT_GELU = 2 /* exact */ } prism_activation;
+
+typedef struct {
+    int N, S, C, G;        /* samples, positions, channels, groups (G divides C)                  */
+    prism_dtype io;        /* type of x, gate, y and of their gradients (the rest is fp32)        */
+    prism_activation act;
+    float eps;             /* >= 0                                                                */
+} prism_norm_shape;
+
+/* prism_group_norm_fwd_workspace_size -- bytes of device workspace prism_group_norm_fwd needs for
+ * `shape`.  Depends on the current device's SM count.  Writes *bytes. */
+prism_status prism_group_norm_fwd_workspace_size(const prism_norm_shape *shape, size_t *bytes);
+
+/*
+ * prism_group_norm_fwd --
+ *   x, gate      [N,S,C] io         gate may be NULL
+ *   weight, bias [C] fp32           each may be NULL (1 and 0)
+ *   y            [N,S,C] io         output
+ *   mean, rstd   [N,G] fp32         outputs for prism_group_norm_bwd, each may be NULL
+ *   workspace, ws_bytes             at least prism_group_norm_fwd_workspace_size bytes, 256-byte
+ *                                   aligned; needs no clearing
+ * x, gate and y dense and 16-byte aligned, the others 4-byte aligned; no output may overlap an
+ * input or another output.  C <= 2^20, N <= 2^24, N*G < 2^31.  All arithmetic in fp32, y rounded
+ * once.  With N or S of zero nothing is written.
+ */
+prism_status prism_group_norm_fwd(const prism_norm_shape *shape, const void *x, const float *weight,
+                                  const float *bias, const void *gate, void *y, float *mean,
+                                  float *rstd, void *workspace, size_t ws_bytes, void *stream);
+
+/* prism_group_norm_bwd_workspace_size -- bytes of device workspace prism_group_norm_bwd needs for
+ * `shape`.  Depends on the current device's SM count.  Writes *bytes. */
+prism_status prism_group_norm_bwd_workspace_size(const prism_norm_shape *shape, size_t *bytes);
+
+/*
+ * prism_group_norm_bwd -- gradients of prism_group_norm_fwd.
+ *   x, weight, bias, gate, mean, rstd   as passed to and returned by prism_group_norm_fwd
+ *   dy              [N,S,C] io          upstream gradient of y
+ *   dx              [N,S,C] io          output
+ *   dgate           [N,S,C] io          output; given exactly if gate is
+ *   dweight, dbias  [C] fp32            outputs, each may be NULL (not computed)
+ *   workspace, ws_bytes                 at least prism_group_norm_bwd_workspace_size bytes, 256-byte
+ *                                       aligned; needs no clearing
+ * Alignment, overlap and limits as for prism_group_norm_fwd.  eps is not used.  dweight and dbias
+ * are summed in a fixed order (no atomics).  With N or S of zero dweight and dbias are zero.
+ */
+prism_status prism_group_norm_bwd(const prism_norm_shape *shape, const void *x, const float *weight,
+                                  const float *bias, const void *gate, const float *mean,
+                                  const float *rstd, const void *dy, void *dx, void *dgate,
+                                  float *dweight, float *dbias, void *workspace, size_t ws_bytes,
+                                  void *stream);
+
+/*
  * prism_query_device_status -- synchronise `stream`, read the status word in `workspace` (written
  * by scan kernels whose bounded waits ran out; workspace may be NULL) and the library's own
  * status words on the current device (decode, producer, and the scratch of
