@@ -26,6 +26,7 @@ cudaError_t launch_segment_element(const ScanArgs &a, int route, bool io_f32, vo
 cudaError_t launch_state_fold(int BH, int dk, int dv, const float *S_in, const float *E, const float *f,
                               float *S_out, cudaStream_t s);
 cudaError_t noalloc_status(uint32_t *out);
+cudaError_t decay_status(uint32_t *out);
 size_t bwd_workspace_bytes(int B, int H, int T, int dk, int dv, bool io_f32);
 cudaError_t launch_scan_bwd(const ScanArgs &f, const void *dO, const float *dS_final, float *dq,
                             float *dk, float *dv, float *dalpha, float *dbeta, float *du, float *dw,
@@ -419,13 +420,15 @@ prism_status prism_query_device_status(void *workspace, void *stream) {
         if (word != PRISM_OK && (err = cudaMemset(workspace, 0, sizeof word)) != cudaSuccess)
             return cuda_status(err);
     }
-    uint32_t dword = 0, pword = 0, nword = 0;
+    uint32_t dword = 0, pword = 0, nword = 0, cword = 0;
     if ((err = prism::decode_status(&dword)) != cudaSuccess) return cuda_status(err);
     if ((err = prism::producer_status(&pword)) != cudaSuccess) return cuda_status(err);
     if ((err = prism::noalloc_status(&nword)) != cudaSuccess) return cuda_status(err);
+    if ((err = prism::decay_status(&cword)) != cudaSuccess) return cuda_status(err);
     if (word == PRISM_OK) word = dword;
     if (word == PRISM_OK) word = pword;
     if (word == PRISM_OK) word = nword;
+    if (word == PRISM_OK) word = cword;
     return (prism_status)word;
 }
 

@@ -51,6 +51,7 @@ struct DecayPass {
     float *F;             // sum kernel's output, [B, H, nseg] matrices [d2][d1]
     int reverse;
     int nseg, seg_tokens; // segments per sequence, tokens per segment (whole chunks)
+    int stall;            // the give-up test: no load is issued, every wait runs out after a short limit
 };
 
 // Valid tokens of sequence b.
@@ -68,10 +69,14 @@ __device__ __forceinline__ float decay_pow(float a, int n) {
     return (float)exp2((double)n * log2((double)a));
 }
 
-constexpr int kDecayChunkSimt = 64;
+constexpr int kDecayChunkSimt = 64, kDecayChunkTc = 128;  // tokens of a chunk
 
-cudaError_t launch_decay_sum_simt(const DecayPass &p, bool io_f32, cudaStream_t s);
-cudaError_t launch_decay_pass_simt(const DecayPass &p, bool io_f32, cudaStream_t s);
+// fp32 operands, on CUDA cores; bf16 operands, on the tensor cores.
+cudaError_t launch_decay_sum_simt(const DecayPass &p, cudaStream_t s);
+cudaError_t launch_decay_pass_simt(const DecayPass &p, cudaStream_t s);
+cudaError_t launch_decay_sum_tc(const DecayPass &p, cudaStream_t s);
+cudaError_t launch_decay_pass_tc(const DecayPass &p, cudaStream_t s);
+cudaError_t decay_status(uint32_t *out);  // read and clear the tensor-core kernels' status word
 
 // Entry states of every segment from the segments' sums, in place of them, and the exit state.
 struct DecayCarry {

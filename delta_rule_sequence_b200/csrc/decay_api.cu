@@ -8,6 +8,9 @@
 namespace prism {
 namespace {
 
+// prism_debug_set_flags bit 8: the stall test of the tensor-core kernels.
+constexpr int kDebugStallDecay = 256;
+
 size_t io_bytes(prism_dtype io) { return io == PRISM_F32 ? 4 : 2; }
 
 // One operand as the kernels read it, and the bytes from its first to behind its last element.
@@ -71,7 +74,7 @@ struct DecayPlan {
 constexpr int kStart = 2;
 
 DecayPlan plan_of(const prism_decay_shape &s) {
-    const int chunk = kDecayChunkSimt;
+    const int chunk = s.io == PRISM_F32 ? kDecayChunkSimt : kDecayChunkTc;
     const int nch = std::max(1, (s.T + chunk - 1) / chunk);
     const long long bh = std::max(1LL, (long long)s.B * s.H);
     const int sms = sm_count();
@@ -119,7 +122,8 @@ struct Runner {
         p.B = s.B; p.H = s.H; p.T = s.T; p.d1 = d1; p.d2 = d2;
         p.y = y; p.z = z; p.decay = decay; p.lengths = lengths;
         p.F = F; p.reverse = reverse; p.nseg = pl.nseg; p.seg_tokens = pl.seg_tokens;
-        err = launch_decay_sum_simt(p, f32(), stream);
+        p.stall = (debug_flags() & kDebugStallDecay) != 0;
+        err = f32() ? launch_decay_sum_simt(p, stream) : launch_decay_sum_tc(p, stream);
     }
     void carry(float *F, const float *init, float *final_state, bool reverse) {
         if (err != cudaSuccess) return;
@@ -134,7 +138,8 @@ struct Runner {
         p.x = x; p.y = y; p.z = z; p.decay = decay; p.lengths = lengths;
         p.entry = entry; p.entry_t = entry_t; p.reverse = reverse; p.o = o; p.o_f32 = o_f32;
         p.nseg = pl.nseg; p.seg_tokens = pl.seg_tokens;
-        err = launch_decay_pass_simt(p, f32(), stream);
+        p.stall = (debug_flags() & kDebugStallDecay) != 0;
+        err = f32() ? launch_decay_pass_simt(p, stream) : launch_decay_pass_tc(p, stream);
     }
     // a state without tokens: out = init or zero
     void copy_state(float *out, const float *init) {

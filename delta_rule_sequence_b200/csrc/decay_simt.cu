@@ -1,6 +1,6 @@
 // decay_simt.cu -- the decay scan's kernels on CUDA cores, in fp32 throughout (decay.cuh has the
-// formulas): the segment sums, the pass over the tokens, the carry between segments and the sum of
-// shared heads' gradients.
+// formulas): the segment sums and the pass over the tokens for fp32 operands, the carry between
+// segments and the sum of shared heads' gradients for both types.
 
 #include "decay.cuh"
 
@@ -13,25 +13,14 @@ constexpr int NT = 256;              // 16 x 16 threads
 // Tile rows [t0, t0 + CH) of one head into shared memory as fp32, zero beyond `len` tokens and beyond
 // the operand's own width d (tiles are D = 64 or 128 columns wide, rows D + 4 floats apart: 16-byte
 // aligned, and 16 rows read at one column fall into different banks).
-template <typename IO, int D>
+template <int D>
 __device__ __forceinline__ void load_tile(float *dst, const DecayTensor &x, int b, int h, int t0, int len, int d) {
-    constexpr int V = 16 / sizeof(IO);  // elements of a 16-byte load (d is a multiple of 32)
-    const IO *src = (const IO *)x.p + b * x.sb + (long long)(h / x.div) * x.sh;
-    for (int e = threadIdx.x; e < CH * (D / V); e += NT) {
-        const int r = e / (D / V), c = (e % (D / V)) * V;
-        float f[V];
-        if (t0 + r < len && c < d) {
-            const uint4 raw = *reinterpret_cast<const uint4 *>(src + (long long)(t0 + r) * x.st + c);
-            const IO *v = reinterpret_cast<const IO *>(&raw);
-#pragma unroll
-            for (int i = 0; i < V; ++i) f[i] = ld_io(v, i);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) f[i] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < V; i += 4)
-            *reinterpret_cast<float4 *>(dst + r * (D + 4) + c + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+    const float *src = (const float *)x.p + b * x.sb + (long long)(h / x.div) * x.sh;
+    for (int e = threadIdx.x; e < CH * (D / 4); e += NT) {
+        const int r = e / (D / 4), c = (e % (D / 4)) * 4;  // (d is a multiple of 32)
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t0 + r < len && c < d) f = *reinterpret_cast<const float4 *>(src + (long long)(t0 + r) * x.st + c);
+        *reinterpret_cast<float4 *>(dst + r * (D + 4) + c) = f;
     }
 }
 
@@ -65,7 +54,7 @@ __device__ __forceinline__ int tile_col(int i, int t) { return 64 * (i >> 2) + 4
 __device__ __forceinline__ int write_exponent(int j, int n, int reverse) { return reverse ? j + 1 : n - 1 - j; }
 
 // F[n][m] of one segment: the state that its tokens alone leave behind.
-template <typename IO, int D1, int D2>
+template <int D1, int D2>
 __global__ void __launch_bounds__(NT) decay_sum_simt_kernel(DecayPass p) {
     extern __shared__ __align__(16) float sm[];
     float *Y = sm, *Z = Y + CH * (D1 + 4), *pw = Z + CH * (D2 + 4), *w = pw + CH + 1;
@@ -81,8 +70,8 @@ __global__ void __launch_bounds__(NT) decay_sum_simt_kernel(DecayPass p) {
         const int t0 = s0 + (p.reverse ? nch - 1 - cc : cc) * CH;
         const int n = min(CH, s1 - t0);
         __syncthreads();
-        load_tile<IO, D1>(Y, p.y, b, h, t0, len, p.d1);
-        load_tile<IO, D2>(Z, p.z, b, h, t0, len, p.d2);
+        load_tile<D1>(Y, p.y, b, h, t0, len, p.d1);
+        load_tile<D2>(Z, p.z, b, h, t0, len, p.d2);
         for (int j = threadIdx.x; j < CH; j += NT) w[j] = j < n ? pw[write_exponent(j, n, p.reverse)] : 0.f;
         const float an = pw[n];
 #pragma unroll
@@ -107,7 +96,7 @@ __global__ void __launch_bounds__(NT) decay_sum_simt_kernel(DecayPass p) {
 
 // One segment's outputs, chunk by chunk, the state in shared memory (R^T: rows along y, so that the
 // entry term X R^T reads like the P Z product).
-template <typename IO, int D1, int D2>
+template <int D1, int D2>
 __global__ void __launch_bounds__(NT) decay_pass_simt_kernel(DecayPass p) {
     extern __shared__ __align__(16) float sm[];
     constexpr int PP = CH + 4;
@@ -130,17 +119,16 @@ __global__ void __launch_bounds__(NT) decay_pass_simt_kernel(DecayPass p) {
     }
     auto store = [&](int t, int n, float x) {
         const long long at = (((long long)b * p.T + t) * p.H + h) * p.d2 + n;
-        if (p.o_f32) ((float *)p.o)[at] = x;
-        else st_io((IO *)p.o, at, x);
+        ((float *)p.o)[at] = x;
     };
     const int nch = s1 > s0 ? (s1 - s0 + CH - 1) / CH : 0;
     for (int cc = 0; cc < nch; ++cc) {
         const int t0 = s0 + (p.reverse ? nch - 1 - cc : cc) * CH;
         const int n = min(CH, s1 - t0);
         __syncthreads();
-        load_tile<IO, D1>(X, p.x, b, h, t0, len, p.d1);
-        load_tile<IO, D1>(Y, p.y, b, h, t0, len, p.d1);
-        load_tile<IO, D2>(Z, p.z, b, h, t0, len, p.d2);
+        load_tile<D1>(X, p.x, b, h, t0, len, p.d1);
+        load_tile<D1>(Y, p.y, b, h, t0, len, p.d1);
+        load_tile<D2>(Z, p.z, b, h, t0, len, p.d2);
         for (int j = threadIdx.x; j < CH; j += NT) w[j] = j < n ? pw[write_exponent(j, n, p.reverse)] : 0.f;
         __syncthreads();
         // P[i][j] = a^|i-j| x_i . y_j on the causal side, rows i = ty + 16 r, columns j = tx + 16 c
@@ -244,11 +232,11 @@ __global__ void __launch_bounds__(NT) decay_pass_simt_kernel(DecayPass p) {
     for (int e = threadIdx.x; e < (send - z0) * p.d2; e += NT) store(z0 + e / p.d2, e % p.d2, 0.f);
 }
 
-template <typename IO, int D1, int D2>
+template <int D1, int D2>
 cudaError_t launch_one(const DecayPass &p, bool sum, cudaStream_t s) {
     const int tiles = CH * (D1 + 4) + CH * (D2 + 4) + CH + 1 + CH;
     const int bytes = 4 * (sum ? tiles : tiles + CH * (D1 + 4) + D1 * (D2 + 4) + CH * (CH + 4));
-    auto kern = sum ? decay_sum_simt_kernel<IO, D1, D2> : decay_pass_simt_kernel<IO, D1, D2>;
+    auto kern = sum ? decay_sum_simt_kernel<D1, D2> : decay_pass_simt_kernel<D1, D2>;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (err != cudaSuccess) return err;
     launch_probe_mark(s);
@@ -256,10 +244,9 @@ cudaError_t launch_one(const DecayPass &p, bool sum, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-template <typename IO>
 cudaError_t launch_widths(const DecayPass &p, bool sum, cudaStream_t s) {
-    if (p.d1 <= 64) return p.d2 <= 64 ? launch_one<IO, 64, 64>(p, sum, s) : launch_one<IO, 64, 128>(p, sum, s);
-    return p.d2 <= 64 ? launch_one<IO, 128, 64>(p, sum, s) : launch_one<IO, 128, 128>(p, sum, s);
+    if (p.d1 <= 64) return p.d2 <= 64 ? launch_one<64, 64>(p, sum, s) : launch_one<64, 128>(p, sum, s);
+    return p.d2 <= 64 ? launch_one<128, 64>(p, sum, s) : launch_one<128, 128>(p, sum, s);
 }
 
 // One thread per state element walks the segments in order: entry states replace the sums.
@@ -300,13 +287,8 @@ __global__ void decay_group_sum_kernel(const float *part, IO *out, long long tot
 
 }  // namespace
 
-cudaError_t launch_decay_sum_simt(const DecayPass &p, bool io_f32, cudaStream_t s) {
-    return io_f32 ? launch_widths<float>(p, true, s) : launch_widths<__nv_bfloat16>(p, true, s);
-}
-
-cudaError_t launch_decay_pass_simt(const DecayPass &p, bool io_f32, cudaStream_t s) {
-    return io_f32 ? launch_widths<float>(p, false, s) : launch_widths<__nv_bfloat16>(p, false, s);
-}
+cudaError_t launch_decay_sum_simt(const DecayPass &p, cudaStream_t s) { return launch_widths(p, true, s); }
+cudaError_t launch_decay_pass_simt(const DecayPass &p, cudaStream_t s) { return launch_widths(p, false, s); }
 
 cudaError_t launch_decay_carry(const DecayCarry &c, cudaStream_t s) {
     launch_probe_mark(s);

@@ -1,0 +1,657 @@
+// decay_tc.cu -- the decay scan's bf16 kernels on the tensor cores (decay.cuh has the formulas): the
+// segment sums and the pass over the tokens, chunks of 128 tokens, one CTA per segment of one (b, h).
+//
+// Per chunk, with n tokens, weights w_j of the state's write and row factors f_i of its read:
+//   P   = X Y^T                 [128 tokens x 128 tokens]   M = 128, N = 128, K = D1
+//   O   = f o (X R^T) + P' Z    P' = a^|i-j| P on the causal side, rounded to bf16
+//   dR^T = (w o Y)^T Z          [D1 x D2], the write; R^T <- a^n R^T + dR^T in fp32 registers
+// Operands that come from registers (P', the weighted Y) go to the tensor core through TMEM, where the
+// A operand's row is the lane: no shared memory and no swizzle.  The weighted Y is not rounded to one bf16: a
+// state sums thousands of them.  It is split into bf16 terms whose sum has 16 (pass kernel: only outputs
+// depend on it) or 24 bits (sum kernel: the fp32 states that the caller gets), each multiplied with the exact Z.
+// The state is rounded to bf16 once per chunk as the B operand of X R^T; its fp32 master stays in
+// registers, so that no tensor-core accumulation runs longer than one chunk.
+//
+// Widths of 32 run as 64: the TMA boxes reach past the tensor, where loads give zeros and stores
+// write nothing.
+
+#include "decay.cuh"
+#include "tc.cuh"
+#include "tensor_map.cuh"
+
+namespace prism {
+namespace {
+
+using namespace tc;
+
+constexpr int CT = kDecayChunkTc;
+
+// Library status word of these kernels (a bounded wait that gave up), read and cleared by
+// prism_query_device_status.
+__device__ uint32_t g_decay_status;
+
+struct DecayMaps {
+    CUtensorMap x, y, z, o;
+};
+
+// Bytes of a tile of 128 tokens, D columns (64-column blocks of 128 rows x 128 bytes).
+constexpr uint32_t kBlk = CT * 128;
+template <int D>
+constexpr uint32_t tile_bytes() { return kBlk * (D / 64); }
+
+// What a CTA works on: segment `seg` of sequence (b, h); chunk i of its walk starts at token t0(i) and
+// has n(i) valid tokens.
+struct Walk {
+    int b, h, seg, len, s0, s1, send, nch, reverse;
+    __device__ explicit Walk(const DecayPass &p) {
+        seg = blockIdx.x;
+        h = blockIdx.y;
+        b = blockIdx.z;
+        len = decay_len(p.lengths, b, p.T);
+        s0 = seg * p.seg_tokens;
+        send = min(s0 + p.seg_tokens, p.T);
+        s1 = min(send, len);
+        nch = s1 > s0 ? (s1 - s0 + CT - 1) / CT : 0;
+        reverse = p.reverse;
+    }
+    __device__ int t0(int i) const { return s0 + (reverse ? nch - 1 - i : i) * CT; }
+    __device__ int n(int i) const { return min(CT, s1 - t0(i)); }
+};
+
+__device__ __forceinline__ void load_tile(uint8_t *dst, const CUtensorMap *m, int D, int head, int t, int b, uint64_t *bar) {
+    mbar_expect_tx(bar, kBlk * (D / 64));
+    for (int c = 0; c < D / 64; ++c) tma_load_4d(dst + c * kBlk, m, 64 * c, head, t, b, bar);
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) { return pack_bf16(a, b); }
+__device__ __forceinline__ float lo_f(uint32_t p) { return __uint_as_float(p << 16); }
+__device__ __forceinline__ float hi_f(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
+
+// Powers of a head's decay in shared memory: p[CT + e] = a^e for 0 <= e <= CT, zero below.
+struct Powers {
+    float p[2 * CT + 1];
+    __device__ void fill(float a, int tid, int nthreads) {
+        for (int i = tid; i <= 2 * CT; i += nthreads) p[i] = i < CT ? 0.f : decay_pow(a, i - CT);
+    }
+    __device__ __forceinline__ float at(int e) const { return p[CT + e]; }
+};
+
+// Column m of the Y tile, tokens j0 .. j0 + 31, times their weights in the state that leaves a chunk of
+// n valid tokens (a^(n - 1 - j), reversed a^(j + 1)), as TERMS bf16 terms into this thread's TMEM lane:
+// term t at column col + 64 t, two tokens per column.  Tokens beyond n are zero whatever the tile holds.
+template <int TERMS>
+__device__ __forceinline__ void weigh32(const uint8_t *Y, int m, const Powers &pw, int j0, int n, int reverse,
+                                        uint32_t taddr_lane, int col) {
+    const float *w = pw.p + CT + (reverse ? 1 : n - 1);
+    const int step = reverse ? 1 : -1;
+    uint32_t t[TERMS][16];
+    const uint8_t *base = Y + (m >> 6) * kBlk + ((m & 7) << 1);
+    const int ch = (m & 63) >> 3;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float x[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int j = j0 + 2 * i + e;
+            const uint32_t raw = *reinterpret_cast<const uint16_t *>(base + j * 128 + ((ch ^ (j & 7)) << 4));
+            x[e] = j < n ? __uint_as_float(raw << 16) * w[step * j] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < TERMS; ++k) {
+            t[k][i] = bf16_pair(x[0], x[1]);
+            x[0] -= lo_f(t[k][i]);
+            x[1] -= hi_f(t[k][i]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < TERMS; ++k) tmem_st16(taddr_lane + col + 64 * k + j0 / 2, t[k]);
+}
+
+// Zero rows n .. 127 of a tile (by `nthreads` threads), so that what lies behind the sequence's end
+// reaches no product.
+template <int D>
+__device__ __forceinline__ void zero_rows(uint8_t *tile, int n, int tid, int nthreads) {
+    for (int e = tid; e < (CT - n) * (D / 64) * 8; e += nthreads) {
+        const int c = e & 7, blk = (e >> 3) % (D / 64), r = n + (e >> 3) / (D / 64);
+        *reinterpret_cast<uint4 *>(tile + blk * kBlk + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+    }
+}
+
+// ------------------------------------------------------------------------------------------------
+// Segment sums.  Per chunk three products of 128 x D2 x 128 against 2 tiles of loads: the loads are
+// the bound (at D1 = D2 = 128 about 2700 cycles a chunk at the copy bandwidth, the products 1536).
+
+template <int D1, int D2>
+struct SumLayout {
+    static constexpr int YW = 8, SW = 8;                 // warps that weigh Y, that hold the state
+    static constexpr int LOADW = YW + SW, MMAW = LOADW + 1;
+    static constexpr int THREADS = 32 * (MMAW + 1);
+    static constexpr int NST = 227 * 1024 / (tile_bytes<D1>() + tile_bytes<D2>() + 1024) > 4 ? 4 : 3;
+    static constexpr uint32_t STAGE = tile_bytes<D1>() + tile_bytes<D2>();
+    static constexpr uint32_t BYTES = NST * STAGE + 1024;
+    static constexpr uint32_t cY = 0, cD = 384;          // TMEM: two buffers of three terms, the product
+    static_assert(BYTES <= 227 * 1024, "shared memory budget");
+};
+
+template <int D1, int D2>
+__global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
+    decay_sum_tc_kernel(DecayPass p, const __grid_constant__ DecayMaps maps) {
+    using LY = SumLayout<D1, D2>;
+    constexpr int NST = LY::NST;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    __shared__ uint64_t full[NST], freeb[NST], yp_full[2], yp_free[2], d_full, d_free, drain;
+    __shared__ Powers pw;
+    __shared__ uint32_t tmem_base_sh;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Walk wk(p);
+    uint32_t *status = &g_decay_status;
+    const uint32_t lim = p.stall ? kStallTestPolls : kWaitPolls;
+    const float a = p.decay[wk.h];
+
+    if (warp == LY::MMAW) tmem_alloc(&tmem_base_sh, 512);
+    if (tid == 0) {
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&freeb[i], LY::YW + 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&yp_full[i], LY::YW);
+            mbar_init(&yp_free[i], 1);
+        }
+        mbar_init(&d_full, 1);
+        mbar_init(&d_free, LY::SW);
+        mbar_init(&drain, 1);
+        mbar_fence_init();
+    }
+    pw.fill(a, tid, LY::THREADS);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tb = tmem_base_sh;
+
+    if (warp == LY::LOADW) {
+        if (lane == 0 && !p.stall) {
+            int i = 0;
+            for (; i < wk.nch; ++i) {
+                const int st = i % NST;
+                if (i >= NST && !mbar_wait(&freeb[st], (uint32_t)((i / NST - 1) & 1), status, lim)) break;
+                uint8_t *s = sm + st * LY::STAGE;
+                mbar_expect_tx(&full[st], LY::STAGE);
+                for (int c = 0; c < D1 / 64; ++c) tma_load_4d(s + c * kBlk, &maps.y, 64 * c, wk.h / p.y.div, wk.t0(i), wk.b, &full[st]);
+                for (int c = 0; c < D2 / 64; ++c)
+                    tma_load_4d(s + tile_bytes<D1>() + c * kBlk, &maps.z, 64 * c, wk.h / p.z.div, wk.t0(i), wk.b, &full[st]);
+            }
+            // loads in flight land before the CTA exits
+            for (int k = i > NST ? i - NST : 0; k < i; ++k) mbar_wait(&full[k % NST], (uint32_t)((k / NST) & 1), nullptr, lim);
+        }
+    } else if (warp == LY::MMAW) {
+        if (lane == 0) {
+            const uint32_t id = idesc_bf16(128, D2, 0, 1);
+            auto oz = [](int ks) { return (uint64_t)koff_mn_sw128(ks); };
+            for (int i = 0; i < wk.nch; ++i) {
+                const int st = i % NST, pb = i & 1;
+                if (!mbar_wait(&full[st], (uint32_t)((i / NST) & 1), status, lim) ||
+                    !mbar_wait(&yp_full[pb], (uint32_t)((i >> 1) & 1), status, lim) ||
+                    (i > 0 && !mbar_wait(&d_free, (uint32_t)((i - 1) & 1), status, lim)))
+                    break;
+                fence_after_sync();
+                const uint64_t dz = make_desc(smem_u32(sm + st * LY::STAGE + tile_bytes<D1>()), kBlk, 1024, 2);
+                const uint32_t ya = tb + LY::cY + pb * 192;
+                // smallest terms first: their sum loses nothing to the large one's magnitude
+                mma_steps_tmem_a<CT / 16>(tb + LY::cD, id, ya + 128, dz, oz, false);
+                mma_steps_tmem_a<CT / 16>(tb + LY::cD, id, ya + 64, dz, oz, true);
+                mma_steps_tmem_a<CT / 16>(tb + LY::cD, id, ya, dz, oz, true);
+                mma_commit(&d_full);
+                mma_commit(&yp_free[pb]);
+                mma_commit(&freeb[st]);
+            }
+            mma_commit(&drain);
+            mbar_wait(&drain, 0, nullptr, lim);
+        }
+    } else if (warp < LY::YW) {
+        const int q = warp & 3, half = warp >> 2, m = 32 * q + lane;
+        for (int i = 0; i < wk.nch; ++i) {
+            const int st = i % NST, pb = i & 1, n = wk.n(i);
+            uint8_t *s = sm + st * LY::STAGE;
+            if (!mbar_wait(&full[st], (uint32_t)((i / NST) & 1), status, lim) ||
+                (i >= 2 && !mbar_wait(&yp_free[pb], (uint32_t)(((i >> 1) - 1) & 1), status, lim)))
+                break;
+            fence_after_sync();
+            if (n < CT) {
+                zero_rows<D2>(s + tile_bytes<D1>(), n, tid, 32 * LY::YW);
+                fence_async_smem();
+            }
+            if (32 * q < D1) {
+                weigh32<3>(s, m, pw, 64 * half, n, wk.reverse, taddr(tb, 32 * q, 0), LY::cY + pb * 192);
+                weigh32<3>(s, m, pw, 64 * half + 32, n, wk.reverse, taddr(tb, 32 * q, 0), LY::cY + pb * 192);
+                tmem_wait_st();
+            }
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&yp_full[pb]);
+                mbar_arrive(&freeb[st]);
+            }
+        }
+    } else {
+        const int sw = warp - LY::YW, q = sw & 3, half = sw >> 2, m = 32 * q + lane;
+        constexpr int NC = D2 / 2;
+        float r[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) r[c] = 0.f;
+        bool ok = true;
+        for (int i = 0; i < wk.nch; ++i) {
+            const float an = pw.at(wk.n(i));
+            if (!mbar_wait(&d_full, (uint32_t)(i & 1), status, lim)) { ok = false; break; }
+            fence_after_sync();
+            if (32 * q < D1) {
+#pragma unroll
+                for (int c = 0; c < NC; c += 32) {
+                    float d[32];
+                    tmem_ld32(taddr(tb, 32 * q, LY::cD + half * NC + c), d);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) r[c + k] = fmaf(an, r[c + k], d[k]);
+                }
+            }
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&d_free);
+        }
+        if (ok && m < p.d1) {
+            float *F = p.F + (((long long)wk.b * p.H + wk.h) * p.nseg + wk.seg) * p.d1 * p.d2 + m;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const int nn = half * NC + c;
+                if (nn < p.d2) F[nn * p.d1] = r[c];
+            }
+        }
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    if (warp == LY::MMAW) tmem_dealloc(tb, 512);
+}
+
+// ------------------------------------------------------------------------------------------------
+// The pass.
+
+template <int D1, int D2>
+struct PassLayout {
+    static constexpr int PW = 4, OW = 4, SW = 8, YW = 4;  // warps: P', outputs, state, weighted Y
+    static constexpr int OW0 = PW, SW0 = OW0 + OW, YW0 = SW0 + SW, LOADW = YW0 + YW, MMAW = LOADW + 1;
+    static constexpr int THREADS = 32 * (MMAW + 1);
+    static constexpr int NST = D1 == 64 ? (D2 == 64 ? 4 : 3) : 2;
+    static constexpr uint32_t X = 0, Y = tile_bytes<D1>(), Z = 2 * tile_bytes<D1>();
+    static constexpr uint32_t STAGE = 2 * tile_bytes<D1>() + tile_bytes<D2>();
+    static constexpr uint32_t R = NST * STAGE;            // R^T as bf16: rows along y, columns along z
+    static constexpr uint32_t R_BLK = D1 * 128;
+    static constexpr uint32_t BYTES = R + R_BLK * (D2 / 64) + 1024;
+    static constexpr uint32_t cP = 0, cO = 128, cD = 128 + D2, cY = 128 + 2 * D2;  // TMEM columns
+    static_assert(BYTES + 1024 <= 227 * 1024, "shared memory budget");
+    static_assert(cY + 128 <= 512, "TMEM columns");
+};
+
+template <int D1, int D2>
+__global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
+    decay_pass_tc_kernel(DecayPass p, const __grid_constant__ DecayMaps maps) {
+    using LY = PassLayout<D1, D2>;
+    constexpr int NST = LY::NST;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    __shared__ uint64_t x_full[NST], y_full[NST], z_full[NST], x_free[NST], y_free[NST], z_free[NST];
+    __shared__ uint64_t p_full, p_ready, qs_full, o_scaled, o_full, o_free, s_ready, ds_full, yp_full, yp_free, drain;
+    __shared__ Powers pw;
+    __shared__ uint32_t tmem_base_sh;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Walk wk(p);
+    uint32_t *status = &g_decay_status;
+    const uint32_t lim = p.stall ? kStallTestPolls : kWaitPolls;
+    const float a = p.decay[wk.h];
+
+    if (warp == LY::MMAW) tmem_alloc(&tmem_base_sh, 512);
+    if (tid == 0) {
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(&x_full[i], 1);
+            mbar_init(&y_full[i], 1);
+            mbar_init(&z_full[i], 1);
+            mbar_init(&x_free[i], 1);
+            mbar_init(&y_free[i], LY::YW + 1);
+            mbar_init(&z_free[i], LY::OW);
+        }
+        mbar_init(&p_full, 1);
+        mbar_init(&p_ready, LY::PW);
+        mbar_init(&qs_full, 1);
+        mbar_init(&o_scaled, LY::OW);
+        mbar_init(&o_full, 1);
+        mbar_init(&o_free, LY::OW);
+        mbar_init(&s_ready, LY::SW);
+        mbar_init(&ds_full, 1);
+        mbar_init(&yp_full, LY::YW);
+        mbar_init(&yp_free, 1);
+        mbar_init(&drain, 1);
+        mbar_fence_init();
+    }
+    pw.fill(a, tid, LY::THREADS);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tb = tmem_base_sh;
+
+    if (warp == LY::LOADW) {
+        if (lane == 0 && !p.stall) {
+            int i = 0;
+            bool ok = true;
+            int nx = 0, ny = 0, nz = 0;  // tiles requested
+            for (; i < wk.nch && ok; ++i) {
+                const int st = i % NST;
+                const uint32_t par = (uint32_t)((i / NST - 1) & 1);
+                uint8_t *s = sm + st * LY::STAGE;
+                if (i >= NST && !mbar_wait(&x_free[st], par, status, lim)) { ok = false; break; }
+                load_tile(s + LY::X, &maps.x, D1, wk.h / p.x.div, wk.t0(i), wk.b, &x_full[st]);
+                ++nx;
+                if (i >= NST && !mbar_wait(&y_free[st], par, status, lim)) { ok = false; break; }
+                load_tile(s + LY::Y, &maps.y, D1, wk.h / p.y.div, wk.t0(i), wk.b, &y_full[st]);
+                ++ny;
+                if (i >= NST && !mbar_wait(&z_free[st], par, status, lim)) { ok = false; break; }
+                load_tile(s + LY::Z, &maps.z, D2, wk.h / p.z.div, wk.t0(i), wk.b, &z_full[st]);
+                ++nz;
+            }
+            // loads in flight land before the CTA exits
+            for (int k = nx > NST ? nx - NST : 0; k < nx; ++k) mbar_wait(&x_full[k % NST], (uint32_t)((k / NST) & 1), nullptr, lim);
+            for (int k = ny > NST ? ny - NST : 0; k < ny; ++k) mbar_wait(&y_full[k % NST], (uint32_t)((k / NST) & 1), nullptr, lim);
+            for (int k = nz > NST ? nz - NST : 0; k < nz; ++k) mbar_wait(&z_full[k % NST], (uint32_t)((k / NST) & 1), nullptr, lim);
+        }
+    } else if (warp == LY::MMAW) {
+        if (lane == 0) {
+            const uint32_t idP = idesc_bf16(128, 128, 0, 0), idZ = idesc_bf16(128, D2, 0, 1);
+            auto ok_ = [](int ks) { return (uint64_t)koff_k_sw128(ks, kBlk); };
+            auto omn = [](int ks) { return (uint64_t)koff_mn_sw128(ks); };
+            const uint64_t dR = make_desc(smem_u32(sm + LY::R), LY::R_BLK, 1024, 2);
+            for (int i = 0; i < wk.nch; ++i) {
+                const int st = i % NST;
+                const uint32_t par = (uint32_t)((i / NST) & 1), ph = (uint32_t)(i & 1), before = (uint32_t)((i - 1) & 1);
+                const uint32_t s = smem_u32(sm + st * LY::STAGE);
+                const uint64_t dX = make_desc(s + LY::X, 16, 1024, 2), dY = make_desc(s + LY::Y, 16, 1024, 2),
+                               dZ = make_desc(s + LY::Z, kBlk, 1024, 2);
+                if (!mbar_wait(&x_full[st], par, status, lim) || !mbar_wait(&y_full[st], par, status, lim)) break;
+                fence_after_sync();
+                // P (its region's last readers were the previous chunk's P' Z products, issued before)
+                mma_steps<D1 / 16>(tb + LY::cP, idP, dX, dY, ok_, ok_, false);
+                mma_commit(&p_full);
+                mma_commit(&y_free[st]);
+                // X R^T
+                if (!mbar_wait(&s_ready, ph, status, lim) || (i > 0 && !mbar_wait(&o_free, before, status, lim))) break;
+                fence_after_sync();
+                mma_steps<D1 / 16>(tb + LY::cO, idZ, dX, dR, ok_, omn, false);
+                mma_commit(&qs_full);
+                mma_commit(&x_free[st]);
+                // the write (the state warps have read the last one: s_ready)
+                if (!mbar_wait(&yp_full, ph, status, lim) || !mbar_wait(&z_full[st], par, status, lim)) break;
+                fence_after_sync();
+                if (i + 1 < wk.nch) {
+                    mma_steps_tmem_a<CT / 16>(tb + LY::cD, idZ, tb + LY::cY + 64, dZ, omn, false);
+                    mma_steps_tmem_a<CT / 16>(tb + LY::cD, idZ, tb + LY::cY, dZ, omn, true);
+                    mma_commit(&ds_full);
+                    mma_commit(&yp_free);
+                }
+                // O += P' Z
+                if (!mbar_wait(&p_ready, ph, status, lim) || !mbar_wait(&o_scaled, ph, status, lim)) break;
+                fence_after_sync();
+                mma_steps_tmem_a<CT / 16>(tb + LY::cO, idZ, tb + LY::cP, dZ, omn, true);
+                mma_commit(&o_full);
+            }
+            mma_commit(&drain);
+            mbar_wait(&drain, 0, nullptr, lim);
+        }
+    } else if (warp < LY::OW0) {
+        // ---------------- P' = a^|i-j| P on the causal side, as bf16 over P's first 64 columns ----------------
+        const int q = warp, row = 32 * q + lane;
+        const uint32_t tl = taddr(tb, 32 * q, LY::cP);
+        for (int i = 0; i < wk.nch; ++i) {
+            const int n = wk.n(i);
+            if (!mbar_wait(&p_full, (uint32_t)(i & 1), status, lim)) break;
+            fence_after_sync();
+#pragma unroll
+            for (int J = 0; J < 4; ++J) {
+                uint32_t out[16];
+                // blocks off the diagonal: a^|row - col| = a^(distance to the block's near column)
+                // x a^(near column - col)
+                if (J == q || (wk.reverse ? J > q : J < q)) {
+                    float v[32];
+                    tmem_ld32(tl + 32 * J, v);
+                    tmem_wait_ld();
+                    if (J == q) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            const int d = wk.reverse ? c - lane : lane - c;
+                            v[c] = d >= 0 ? v[c] * pw.at(d) : 0.f;
+                        }
+                    } else {
+                        const float f = pw.at(wk.reverse ? 32 * J - row : row - 32 * J - 31);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) v[c] = v[c] * f * pw.at(wk.reverse ? c : 31 - c);
+                    }
+                    if (n < CT) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (32 * J + c >= n) v[c] = 0.f;
+                    }
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) out[c] = bf16_pair(v[2 * c], v[2 * c + 1]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) out[c] = 0u;
+                }
+                tmem_st16(tl + 16 * J, out);  // columns that this lane has read already
+            }
+            tmem_wait_st();
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_ready);
+        }
+    } else if (warp < LY::SW0) {
+        // ---------------- outputs ----------------
+        const int q = warp & 3, row = 32 * q + lane;
+        const uint32_t tl = taddr(tb, 32 * q, LY::cO);
+        for (int i = 0; i < wk.nch; ++i) {
+            const int n = wk.n(i), t0 = wk.t0(i), st = i % NST;
+            const bool live = row < n;
+            const float f = live ? pw.at(wk.reverse ? n - 1 - row : row + 1) : 0.f;
+            if (!mbar_wait(&qs_full, (uint32_t)(i & 1), status, lim)) break;
+            fence_after_sync();
+#pragma unroll
+            for (int c = 0; c < D2; c += 32) {
+                float v[32];
+                tmem_ld32(tl + c, v);
+                tmem_wait_ld();
+                uint32_t u[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(v[k] * f);
+                tmem_st32(tl + c, u);
+            }
+            tmem_wait_st();
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_scaled);
+            if (!mbar_wait(&o_full, (uint32_t)(i & 1), status, lim)) break;
+            fence_after_sync();
+            // Z has had its last reader: its rows take the output's
+            uint8_t *zs = sm + st * LY::STAGE + LY::Z;
+#pragma unroll
+            for (int c = 0; c < D2; c += 32) {
+                float v[32];
+                tmem_ld32(tl + c, v);
+                tmem_wait_ld();
+                if (p.o_f32) {
+                    const int t = t0 + row;
+                    if (t < p.T && c < p.d2) {
+                        float *o = (float *)p.o + (((long long)wk.b * p.T + t) * p.H + wk.h) * p.d2 + c;
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            *reinterpret_cast<float4 *>(o + k) = live ? make_float4(v[k], v[k + 1], v[k + 2], v[k + 3])
+                                                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8) {
+                        uint4 u = make_uint4(0, 0, 0, 0);
+                        if (live)
+                            u = make_uint4(bf16_pair(v[k], v[k + 1]), bf16_pair(v[k + 2], v[k + 3]),
+                                           bf16_pair(v[k + 4], v[k + 5]), bf16_pair(v[k + 6], v[k + 7]));
+                        *reinterpret_cast<uint4 *>(zs + sw128_off(row, c + k, kBlk)) = u;
+                    }
+                }
+            }
+            fence_before_sync();
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&o_free);
+                if (!p.o_f32) {
+#pragma unroll
+                    for (int c = 0; c < D2 / 64; ++c)
+                        if (64 * c < p.d2) tma_store_4d(&maps.o, zs + c * kBlk + 32 * q * 128, 64 * c, wk.h, t0 + 32 * q, wk.b);
+                    bulk_commit();
+                    bulk_wait_read();
+                }
+                mbar_arrive(&z_free[st]);
+            }
+        }
+        if (lane == 0) bulk_wait_all();
+    } else if (warp < LY::YW0) {
+        // ---------------- the state: R^T[m][n] of row m = lane, half of the columns ----------------
+        const int sw = warp - LY::SW0, q = sw & 3, half = sw >> 2, m = 32 * q + lane;
+        constexpr int NC = D2 / 2;
+        float r[NC];
+        const float *E = p.entry && m < p.d1
+                             ? p.entry + (((long long)wk.b * p.H + wk.h) * p.nseg + wk.seg) * p.d1 * p.d2 : nullptr;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int nn = half * NC + c;
+            r[c] = E && nn < p.d2 ? (p.entry_t ? E[m * p.d2 + nn] : E[nn * p.d1 + m]) : 0.f;
+        }
+        for (int i = 0; i < wk.nch; ++i) {
+            if (i > 0) {
+                const float an = pw.at(wk.n(i - 1));
+                // the previous chunk's write, and (issued before it) the last read of the bf16 state
+                if (!mbar_wait(&ds_full, (uint32_t)((i - 1) & 1), status, lim)) break;
+                fence_after_sync();
+                if (32 * q < D1) {
+#pragma unroll
+                    for (int c = 0; c < NC; c += 16) {
+                        float d[16];
+                        tmem_ld16(taddr(tb, 32 * q, LY::cD + half * NC + c), d);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) r[c + k] = fmaf(an, r[c + k], d[k]);
+                    }
+                }
+            }
+            if (32 * q < D1) {
+#pragma unroll
+                for (int c = 0; c < NC; c += 8)
+                    *reinterpret_cast<uint4 *>(sm + LY::R + sw128_off(m, half * NC + c, LY::R_BLK)) =
+                        make_uint4(bf16_pair(r[c], r[c + 1]), bf16_pair(r[c + 2], r[c + 3]), bf16_pair(r[c + 4], r[c + 5]),
+                                   bf16_pair(r[c + 6], r[c + 7]));
+            }
+            fence_async_smem();
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_ready);
+        }
+    } else {
+        // ---------------- Y times the write's weights ----------------
+        const int yt = tid - 32 * LY::YW0, q = warp & 3, m = 32 * q + lane;
+        static_assert(LY::YW0 % 4 == 0, "the warp's TMEM lanes");
+        for (int i = 0; i < wk.nch; ++i) {
+            const int st = i % NST, n = wk.n(i);
+            uint8_t *s = sm + st * LY::STAGE;
+            if (!mbar_wait(&y_full[st], (uint32_t)((i / NST) & 1), status, lim)) break;
+            if (n < CT) {
+                if (!mbar_wait(&z_full[st], (uint32_t)((i / NST) & 1), status, lim)) break;
+                zero_rows<D2>(s + LY::Z, n, yt, 32 * LY::YW);
+                fence_async_smem();
+            }
+            // (on the last chunk too, where nothing is written: without it a warp could arrive for this chunk
+            // before another one has for the last, and complete that phase in its place)
+            if (i > 0 && !mbar_wait(&yp_free, (uint32_t)((i - 1) & 1), status, lim)) break;
+            if (i + 1 < wk.nch) {  // (nobody reads the state behind the last chunk)
+                fence_after_sync();
+                if (32 * q < D1) {
+#pragma unroll 1
+                    for (int j0 = 0; j0 < CT; j0 += 32) weigh32<2>(s + LY::Y, m, pw, j0, n, wk.reverse, taddr(tb, 32 * q, 0), LY::cY);
+                    tmem_wait_st();
+                }
+            }
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&yp_full);
+                mbar_arrive(&y_free[st]);
+            }
+        }
+    }
+    // rows behind the sequence's last token
+    const int z0 = max(wk.s0, wk.s1);
+    const int row_bytes = p.d2 * (p.o_f32 ? 4 : 2), per_row = row_bytes / 16;
+    for (int e = tid; e < (wk.send - z0) * per_row; e += LY::THREADS) {
+        const long long t = z0 + e / per_row;
+        *reinterpret_cast<uint4 *>((uint8_t *)p.o + (((long long)wk.b * p.T + t) * p.H + wk.h) * row_bytes + (e % per_row) * 16) =
+            make_uint4(0, 0, 0, 0);
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    if (warp == LY::MMAW) tmem_dealloc(tb, 512);
+}
+
+bool operand_map(CUtensorMap *m, const DecayPass &p, const DecayTensor &t, int d) {
+    return bf16_rows_map(m, t.p, p.B, p.T, p.H / t.div, d, t.sb, t.st, t.sh, CT);
+}
+
+template <int D1, int D2>
+cudaError_t launch_one(const DecayPass &p, bool sum, cudaStream_t s) {
+    DecayMaps maps;
+    bool ok = operand_map(&maps.y, p, p.y, p.d1) && operand_map(&maps.z, p, p.z, p.d2);
+    if (!sum) {
+        ok = ok && operand_map(&maps.x, p, p.x, p.d1);
+        if (!p.o_f32)
+            ok = ok && bf16_rows_map(&maps.o, p.o, p.B, p.T, p.H, p.d2, (long long)p.T * p.H * p.d2, (long long)p.H * p.d2, p.d2, 32);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    const int bytes = sum ? (int)SumLayout<D1, D2>::BYTES : (int)PassLayout<D1, D2>::BYTES;
+    const int threads = sum ? SumLayout<D1, D2>::THREADS : PassLayout<D1, D2>::THREADS;
+    auto kern = sum ? decay_sum_tc_kernel<D1, D2> : decay_pass_tc_kernel<D1, D2>;
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err != cudaSuccess) return err;
+    launch_probe_mark(s);
+    kern<<<dim3(p.nseg, p.H, p.B), threads, bytes, s>>>(p, maps);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_widths(const DecayPass &p, bool sum, cudaStream_t s) {
+    if (p.d1 <= 64) return p.d2 <= 64 ? launch_one<64, 64>(p, sum, s) : launch_one<64, 128>(p, sum, s);
+    return p.d2 <= 64 ? launch_one<128, 64>(p, sum, s) : launch_one<128, 128>(p, sum, s);
+}
+
+}  // namespace
+
+cudaError_t launch_decay_sum_tc(const DecayPass &p, cudaStream_t s) { return launch_widths(p, true, s); }
+cudaError_t launch_decay_pass_tc(const DecayPass &p, cudaStream_t s) { return launch_widths(p, false, s); }
+
+// Read and clear these kernels' status word (PRISM_OK or PRISM_ERR_TIMEOUT).
+cudaError_t decay_status(uint32_t *out) {
+    uint32_t word = 0;
+    cudaError_t err = cudaMemcpyFromSymbol(&word, g_decay_status, sizeof word);
+    if (err != cudaSuccess) return err;
+    if (word != 0) {
+        const uint32_t zero = 0;
+        if ((err = cudaMemcpyToSymbol(g_decay_status, &zero, sizeof zero)) != cudaSuccess) return err;
+    }
+    *out = word;
+    return cudaSuccess;
+}
+
+}  // namespace prism

@@ -392,7 +392,7 @@ prism_status prism_group_norm_bwd(const prism_norm_shape *shape, const void *x, 
 /*
  * prism_query_device_status -- synchronise `stream`, read the status word in `workspace` (written
  * by scan kernels whose bounded waits ran out; workspace may be NULL) and the library's own
- * status words on the current device (decode, producer, and the scratch of
+ * status words on the current device (decode, producer, decay scan, and the scratch of
  * prism_scan_fwd_noalloc), and clear them.  Returns PRISM_OK, PRISM_ERR_TIMEOUT, or
  * PRISM_ERR_CUDA if the stream itself reports an error.
  */
@@ -420,7 +420,8 @@ const char *prism_last_cuda_error(void);
  * test for the per-chunk prep kernels of the tensor-core scan (their tile loads are not issued;
  * PRISM_ERR_TIMEOUT in the workspace status word), for prism_write_producer (its weight loads;
  * the producer status word) and for the bulk-copy decode kernel (its state copies; the decode
- * status word).  Returns the previous flags.
+ * status word); bit 8: the same for the decay scan's tensor-core kernels (their tile loads; the
+ * decay scan's status word).  Returns the previous flags.
  */
 int prism_debug_set_flags(int flags);
 
