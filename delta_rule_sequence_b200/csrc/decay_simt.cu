@@ -249,23 +249,41 @@ cudaError_t launch_widths(const DecayPass &p, bool sum, cudaStream_t s) {
     return p.d2 <= 64 ? launch_one<128, 64>(p, sum, s) : launch_one<128, 128>(p, sum, s);
 }
 
-// One thread per state element walks the segments in order: entry states replace the sums.
-__global__ void decay_carry_kernel(DecayCarry c) {
-    const int bh = blockIdx.x, e = blockIdx.y * blockDim.x + threadIdx.x;
-    const float a = c.decay[bh % c.H];
+// Four state elements per thread, walked over the segments in order: entry states replace the sums.  The
+// sums do not depend on the walk: kAhead of them are loaded at a time.  The two powers a block needs (of a
+// whole segment and of the one that the sequence ends in) are taken once, in 64 bits; taken by every
+// thread they were the kernel's time (32 us instead of 6 for 16 heads of 65536 tokens).
+constexpr int kAhead = 8;
+
+__global__ void __launch_bounds__(128) decay_carry_kernel(DecayCarry c) {
+    __shared__ float pw[2];
+    const int bh = blockIdx.x, e = 4 * (blockIdx.y * 128 + threadIdx.x);
     const int len = decay_len(c.lengths, bh / c.H, c.T);
+    const int last = len / c.seg_tokens, rest = len % c.seg_tokens;  // segment `last` has `rest` tokens
+    if (threadIdx.x < 2) pw[threadIdx.x] = decay_pow(c.decay[bh % c.H], threadIdx.x == 0 ? c.seg_tokens : rest);
+    __syncthreads();
     if (e >= c.elems) return;
-    const float full = decay_pow(a, c.seg_tokens);
-    float *F = c.F + (long long)bh * c.nseg * c.elems + e;
-    float s = c.init ? c.init[(long long)bh * c.elems + e] : 0.f;
-    for (int i = 0; i < c.nseg; ++i) {
-        const int seg = c.reverse ? c.nseg - 1 - i : i;
-        const int n = min(max(len - seg * c.seg_tokens, 0), c.seg_tokens);
-        const float f = F[(long long)seg * c.elems];
-        F[(long long)seg * c.elems] = s;
-        if (n > 0) s = fmaf(n == c.seg_tokens ? full : decay_pow(a, n), s, f);
+    float4 *F = reinterpret_cast<float4 *>(c.F + (long long)bh * c.nseg * c.elems + e);
+    const long long step = c.elems / 4;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c.init) s = *reinterpret_cast<const float4 *>(c.init + (long long)bh * c.elems + e);
+    for (int i0 = 0; i0 < c.nseg; i0 += kAhead) {
+        float4 f[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (i0 + k < c.nseg) f[k] = F[(c.reverse ? c.nseg - 1 - i0 - k : i0 + k) * step];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (i0 + k >= c.nseg) break;
+            const int seg = c.reverse ? c.nseg - 1 - i0 - k : i0 + k;
+            F[seg * step] = s;
+            if (seg < last || (seg == last && rest > 0)) {
+                const float a = pw[seg == last];
+                s = make_float4(fmaf(a, s.x, f[k].x), fmaf(a, s.y, f[k].y), fmaf(a, s.z, f[k].z), fmaf(a, s.w, f[k].w));
+            }
+        }
     }
-    if (c.final_state) c.final_state[(long long)bh * c.elems + e] = s;
+    if (c.final_state) *reinterpret_cast<float4 *>(c.final_state + (long long)bh * c.elems + e) = s;
 }
 
 template <typename IO>
@@ -292,7 +310,7 @@ cudaError_t launch_decay_pass_simt(const DecayPass &p, cudaStream_t s) { return 
 
 cudaError_t launch_decay_carry(const DecayCarry &c, cudaStream_t s) {
     launch_probe_mark(s);
-    decay_carry_kernel<<<dim3(c.BH, (c.elems + 255) / 256), 256, 0, s>>>(c);
+    decay_carry_kernel<<<dim3(c.BH, (c.elems + 511) / 512), 128, 0, s>>>(c);
     return cudaGetLastError();
 }
 

@@ -67,44 +67,57 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) { return pack_bf
 __device__ __forceinline__ float lo_f(uint32_t p) { return __uint_as_float(p << 16); }
 __device__ __forceinline__ float hi_f(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
 
-// Powers of a head's decay in shared memory: p[CT + e] = a^e for 0 <= e <= CT, zero below.
+// Powers of a head's decay in shared memory: at(e) = a^e for 0 <= e <= 128 and 0 for -32 < e < 0, and the
+// weights of a full chunk's tokens in the state that leaves it, w[j] = a^(127 - j), reversed a^(j + 1).
 struct Powers {
-    float p[2 * CT + 1];
-    __device__ void fill(float a, int tid, int nthreads) {
-        for (int i = tid; i <= 2 * CT; i += nthreads) p[i] = i < CT ? 0.f : decay_pow(a, i - CT);
+    alignas(16) float w[CT];
+    alignas(16) float none[32], p[CT + 1];
+    __device__ void fill(float a, int reverse, int tid, int nthreads) {
+        for (int i = tid; i <= CT; i += nthreads) {
+            const float x = decay_pow(a, i);
+            p[i] = x;
+            if (reverse && i > 0) w[i - 1] = x;
+            if (!reverse && i < CT) w[CT - 1 - i] = x;
+            if (i < 32) none[i] = 0.f;
+        }
     }
-    __device__ __forceinline__ float at(int e) const { return p[CT + e]; }
+    __device__ __forceinline__ float at(int e) const { return p[e]; }
 };
 
-// Column m of the Y tile, tokens j0 .. j0 + 31, times their weights in the state that leaves a chunk of
-// n valid tokens (a^(n - 1 - j), reversed a^(j + 1)), as TERMS bf16 terms into this thread's TMEM lane:
-// term t at column col + 64 t, two tokens per column.  Tokens beyond n are zero whatever the tile holds.
+// Column m of the Y tile, tokens j0 .. j0 + 31, times their weights w, as TERMS bf16 terms into this
+// thread's TMEM lane: term t at column col + 64 t, two tokens per column.  Tokens from n on are zero
+// whatever the tile holds there.
 template <int TERMS>
-__device__ __forceinline__ void weigh32(const uint8_t *Y, int m, const Powers &pw, int j0, int n, int reverse,
-                                        uint32_t taddr_lane, int col) {
-    const float *w = pw.p + CT + (reverse ? 1 : n - 1);
-    const int step = reverse ? 1 : -1;
-    uint32_t t[TERMS][16];
+__device__ __forceinline__ void weigh32(const uint8_t *Y, int m, const float *w, int j0, int n, uint32_t taddr_lane, int col) {
     const uint8_t *base = Y + (m >> 6) * kBlk + ((m & 7) << 1);
     const int ch = (m & 63) >> 3;
+    float x[32];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        float x[2];
+    for (int i = 0; i < 32; i += 4) {
+        const float4 w4 = *reinterpret_cast<const float4 *>(w + j0 + i);
+        const float *wf = &w4.x;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int j = j0 + 2 * i + e;
-            const uint32_t raw = *reinterpret_cast<const uint16_t *>(base + j * 128 + ((ch ^ (j & 7)) << 4));
-            x[e] = j < n ? __uint_as_float(raw << 16) * w[step * j] : 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < TERMS; ++k) {
-            t[k][i] = bf16_pair(x[0], x[1]);
-            x[0] -= lo_f(t[k][i]);
-            x[1] -= hi_f(t[k][i]);
+        for (int e = 0; e < 4; ++e) {
+            const int j = i + e;  // (j0 is a multiple of 8: it does not change the swizzle)
+            const uint32_t raw = *reinterpret_cast<const uint16_t *>(base + (j0 + j) * 128 + ((ch ^ (j & 7)) << 4));
+            x[j] = __uint_as_float(raw << 16) * wf[e];
         }
     }
+    if (j0 + 32 > n) {
 #pragma unroll
-    for (int k = 0; k < TERMS; ++k) tmem_st16(taddr_lane + col + 64 * k + j0 / 2, t[k]);
+        for (int j = 0; j < 32; ++j) x[j] = j0 + j < n ? x[j] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < TERMS; ++k) {
+        uint32_t t[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            t[i] = bf16_pair(x[2 * i], x[2 * i + 1]);
+            x[2 * i] -= lo_f(t[i]);
+            x[2 * i + 1] -= hi_f(t[i]);
+        }
+        tmem_st16(taddr_lane + col + 64 * k + j0 / 2, t);
+    }
 }
 
 // Zero rows n .. 127 of a tile (by `nthreads` threads), so that what lies behind the sequence's end
@@ -142,6 +155,7 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     __shared__ uint64_t full[NST], freeb[NST], yp_full[2], yp_free[2], d_full, d_free, drain;
     __shared__ Powers pw;
+    __shared__ __align__(16) float w_last[CT];  // the weights of the walk's last chunk
     __shared__ uint32_t tmem_base_sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Walk wk(p);
@@ -164,11 +178,15 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
         mbar_init(&drain, 1);
         mbar_fence_init();
     }
-    pw.fill(a, tid, LY::THREADS);
+    pw.fill(a, wk.reverse, tid, LY::THREADS);
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
     const uint32_t tb = tmem_base_sh;
+    if (wk.nch > 0)
+        for (int j = tid; j < CT; j += LY::THREADS)
+            w_last[j] = wk.reverse ? pw.w[j] : pw.at(max(wk.n(wk.nch - 1) - 1 - j, 0));
+    __syncthreads();
 
     if (warp == LY::LOADW) {
         if (lane == 0 && !p.stall) {
@@ -223,8 +241,10 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
                 fence_async_smem();
             }
             if (32 * q < D1) {
-                weigh32<3>(s, m, pw, 64 * half, n, wk.reverse, taddr(tb, 32 * q, 0), LY::cY + pb * 192);
-                weigh32<3>(s, m, pw, 64 * half + 32, n, wk.reverse, taddr(tb, 32 * q, 0), LY::cY + pb * 192);
+                const float *w = i + 1 < wk.nch ? pw.w : w_last;
+#pragma unroll 1
+                for (int j0 = 64 * half; j0 < 64 * half + 64; j0 += 32)
+                    weigh32<3>(s, m, w, j0, n, taddr(tb, 32 * q, 0), LY::cY + pb * 192);
                 tmem_wait_st();
             }
             fence_before_sync();
@@ -333,7 +353,7 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
         mbar_init(&drain, 1);
         mbar_fence_init();
     }
-    pw.fill(a, tid, LY::THREADS);
+    pw.fill(a, wk.reverse, tid, LY::THREADS);
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
@@ -413,30 +433,41 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
             const int n = wk.n(i);
             if (!mbar_wait(&p_full, (uint32_t)(i & 1), status, lim)) break;
             fence_after_sync();
-#pragma unroll
+            // 32 columns at a time, in a loop: unrolled, the five roles' code of a chunk no longer fits the
+            // instruction cache and every role waits for its instructions (P' took 7000 cycles instead of 900)
+#pragma unroll 1
             for (int J = 0; J < 4; ++J) {
                 uint32_t out[16];
-                // blocks off the diagonal: a^|row - col| = a^(distance to the block's near column)
-                // x a^(near column - col)
                 if (J == q || (wk.reverse ? J > q : J < q)) {
                     float v[32];
                     tmem_ld32(tl + 32 * J, v);
                     tmem_wait_ld();
                     if (J == q) {
+                        // (the powers of the other side of the diagonal are zeros below the table)
+                        const float *d = pw.p + (wk.reverse ? -lane : lane);
+                        if (wk.reverse) {
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            const int d = wk.reverse ? c - lane : lane - c;
-                            v[c] = d >= 0 ? v[c] * pw.at(d) : 0.f;
+                            for (int c = 0; c < 32; ++c) v[c] *= d[c];
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) v[c] *= d[-c];
                         }
                     } else {
+                        // a^|row - col| = a^(distance to the block's near column) x a^(near column - col)
                         const float f = pw.at(wk.reverse ? 32 * J - row : row - 32 * J - 31);
+                        const float *near = wk.reverse ? pw.p : pw.w + CT - 32;  // a^c, a^(31 - c)
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) v[c] = v[c] * f * pw.at(wk.reverse ? c : 31 - c);
+                        for (int c = 0; c < 32; c += 4) {
+                            const float4 u = *reinterpret_cast<const float4 *>(near + c);
+                            v[c] *= f * u.x;
+                            v[c + 1] *= f * u.y;
+                            v[c + 2] *= f * u.z;
+                            v[c + 3] *= f * u.w;
+                        }
                     }
-                    if (n < CT) {
+                    if (32 * J + 32 > n) {
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (32 * J + c >= n) v[c] = 0.f;
+                        for (int c = 0; c < 32; ++c) v[c] = 32 * J + c < n ? v[c] : 0.f;
                     }
 #pragma unroll
                     for (int c = 0; c < 16; ++c) out[c] = bf16_pair(v[2 * c], v[2 * c + 1]);
@@ -461,7 +492,7 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
             const float f = live ? pw.at(wk.reverse ? n - 1 - row : row + 1) : 0.f;
             if (!mbar_wait(&qs_full, (uint32_t)(i & 1), status, lim)) break;
             fence_after_sync();
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D2; c += 32) {
                 float v[32];
                 tmem_ld32(tl + c, v);
@@ -479,7 +510,7 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
             fence_after_sync();
             // Z has had its last reader: its rows take the output's
             uint8_t *zs = sm + st * LY::STAGE + LY::Z;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D2; c += 32) {
                 float v[32];
                 tmem_ld32(tl + c, v);
@@ -581,7 +612,7 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
                 fence_after_sync();
                 if (32 * q < D1) {
 #pragma unroll 1
-                    for (int j0 = 0; j0 < CT; j0 += 32) weigh32<2>(s + LY::Y, m, pw, j0, n, wk.reverse, taddr(tb, 32 * q, 0), LY::cY);
+                    for (int j0 = 0; j0 < CT; j0 += 32) weigh32<2>(s + LY::Y, m, pw.w, j0, n, taddr(tb, 32 * q, 0), LY::cY);
                     tmem_wait_st();
                 }
             }
