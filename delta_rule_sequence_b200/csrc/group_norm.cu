@@ -16,6 +16,7 @@
 // mean): a mean far above the deviation costs no digits.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "api.cuh"
 #include "common.cuh"
@@ -37,232 +38,384 @@ struct NormArgs {
 
 // ---- activations -------------------------------------------------------------------------------
 
+// Kernels for the common vector widths are built for each activation, with and without a gate (a mode);
+// kRuntime takes both from the arguments.
+constexpr int kRuntime = -1;
+template <int MODE>
+__device__ __forceinline__ int mode_act(const NormArgs &p) { return MODE == kRuntime ? p.act : MODE >> 1; }
+template <int MODE>
+__device__ __forceinline__ bool mode_gate(const NormArgs &p) { return MODE == kRuntime ? p.gate != nullptr : MODE & 1; }
+
+// 1 / x to 1 ulp (0 for infinities: what 1 / (1 + exp(-z)) tends to where exp overflows)
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// __expf for bf16 results: its error, about |x| 2^-24, is far below their rounding.
+template <typename IO>
+__device__ __forceinline__ float exp_io(float x) { return sizeof(IO) == 2 ? __expf(x) : expf(x); }
+
+template <typename IO>
 __device__ __forceinline__ float act_value(int act, float z) {
-    if (act == PRISM_ACT_SILU) return z / (1.f + expf(-z));
+    if (act == PRISM_ACT_SILU) return z * rcp_approx(1.f + exp_io<IO>(-z));
     if (act == PRISM_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
     return z;
 }
 
 // act(z) and act'(z)
+template <typename IO>
 __device__ __forceinline__ float act_both(int act, float z, float &slope) {
     if (act == PRISM_ACT_SILU) {
-        const float s = 1.f / (1.f + expf(-z));
-        slope = s * fmaf(z, 1.f - s, 1.f);
-        return z * s;
+        const float s = rcp_approx(1.f + exp_io<IO>(-z)), a = z * s;
+        slope = fmaf(a, 1.f - s, s);
+        return a;
     }
     if (act == PRISM_ACT_GELU) {
         const float c = 0.5f * (1.f + erff(z * 0.70710678118654752f));
-        slope = fmaf(z * 0.39894228040143268f, expf(-0.5f * z * z), c);
+        slope = fmaf(z * 0.39894228040143268f, exp_io<IO>(-0.5f * z * z), c);
         return z * c;
     }
     slope = 1.f;
     return z;
 }
 
+// ---- arithmetic on a vector's elements, two at a time (packed f32x2) where there are two ----------
+//
+// A unit of one element is a float, of two a 64-bit register pair.
+
+using F2 = unsigned long long;
+template <int V>
+using Unit = std::conditional_t<V == 1, float, F2>;
+template <int V>
+constexpr int kUnits = V == 1 ? 1 : V / 2;
+
+__device__ __forceinline__ F2 pack2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float first(F2 r) { return __uint_as_float((uint32_t)r); }
+__device__ __forceinline__ float second(F2 r) { return __uint_as_float((uint32_t)(r >> 32)); }
+template <typename U>
+__device__ __forceinline__ U both(float x) {
+    if constexpr (sizeof(U) == 4) return x;
+    else return pack2(x, x);
+}
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+    F2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+    F2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+    F2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ float total(float a) { return a; }
+__device__ __forceinline__ float total(F2 a) { return first(a) + second(a); }
+
 // ---- vectors of V consecutive channels -----------------------------------------------------------
 
 template <typename IO, int V>
 struct alignas(sizeof(IO) * V) Pack {
     IO v[V];
+    __device__ __forceinline__ float at(int i) const { return ld_io(v, i); }
+    __device__ __forceinline__ Unit<V> unit(int u) const {
+        if constexpr (V == 1) return at(0);
+        else return pack2(at(2 * u), at(2 * u + 1));
+    }
+    __device__ __forceinline__ void set(int u, float x) { st_io(v, u, x); }
+    __device__ __forceinline__ void set(int u, F2 x) {
+        if constexpr (V > 1) {
+            if constexpr (sizeof(IO) == 2) {
+                reinterpret_cast<__nv_bfloat162 *>(v)[u] = __floats2bfloat162_rn(first(x), second(x));
+            } else {
+                st_io(v, 2 * u, first(x));
+                st_io(v, 2 * u + 1, second(x));
+            }
+        }
+    }
 };
 
 template <typename IO, int V>
-__device__ __forceinline__ void load_vec(const void *p, long long at, float (&f)[V]) {
-    const Pack<IO, V> r = *reinterpret_cast<const Pack<IO, V> *>((const IO *)p + at);
-#pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = ld_io(r.v, i);
+__device__ __forceinline__ Pack<IO, V> load_pack(const void *p, long long at) {
+    return *reinterpret_cast<const Pack<IO, V> *>((const IO *)p + at);
 }
 template <typename IO, int V>
-__device__ __forceinline__ void store_vec(void *p, long long at, const float (&f)[V]) {
-    Pack<IO, V> r;
-#pragma unroll
-    for (int i = 0; i < V; ++i) st_io(r.v, i, f[i]);
+__device__ __forceinline__ void store_pack(void *p, long long at, const Pack<IO, V> &r) {
     *reinterpret_cast<Pack<IO, V> *>((IO *)p + at) = r;
+}
+// Unit u of a channel array (parameters), `missing` where there is none.
+template <int V>
+__device__ __forceinline__ Unit<V> channel_unit(const float *p, int c, float missing) {
+    if constexpr (V == 1) return p ? p[c] : missing;
+    else return p ? pack2(p[c], p[c + 1]) : pack2(missing, missing);
+}
+
+template <typename IO, int MODE>
+__device__ __forceinline__ float y_of(const NormArgs &p, float z, float gate) {
+    return mode_gate<MODE>(p) ? z * act_value<IO>(mode_act<MODE>(p), gate) : act_value<IO>(mode_act<MODE>(p), z);
+}
+template <typename IO, int MODE>
+__device__ __forceinline__ F2 y_of(const NormArgs &p, F2 z, F2 gate) {
+    return pack2(y_of<IO, MODE>(p, first(z), first(gate)), y_of<IO, MODE>(p, second(z), second(gate)));
 }
 
 // dz of one element (before the weight), and its dgate
+template <typename IO, int MODE>
 __device__ __forceinline__ float dz_of(const NormArgs &p, float z, float dy, float gate, float &dgate) {
     float slope;
-    if (p.gate) {
-        const float a = act_both(p.act, gate, slope);
+    if (mode_gate<MODE>(p)) {
+        const float a = act_both<IO>(mode_act<MODE>(p), gate, slope);
         dgate = dy * z * slope;
         return dy * a;
     }
-    act_both(p.act, z, slope);
+    act_both<IO>(mode_act<MODE>(p), z, slope);
+    dgate = 0.f;
     return dy * slope;
+}
+template <typename IO, int MODE>
+__device__ __forceinline__ F2 dz_of(const NormArgs &p, F2 z, F2 dy, F2 gate, F2 &dgate) {
+    float d0, d1;
+    const float a = dz_of<IO, MODE>(p, first(z), first(dy), first(gate), d0);
+    const float b = dz_of<IO, MODE>(p, second(z), second(dy), second(gate), d1);
+    dgate = pack2(d0, d1);
+    return pack2(a, b);
 }
 
 // ---- rows form -----------------------------------------------------------------------------------
 
 constexpr int kRowThreads = 256;
 constexpr int kRowVecs = 4;  // vectors of a lane at most
+constexpr int kRowFwdBlocks = 4, kRowBwdBlocks = 2;  // CTAs of an SM (one vector per lane)
 
 // Sum over the LG lanes of a group (LG a power of two, groups aligned to it).
-__device__ __forceinline__ float lanes_sum(float x, int LG) {
+template <int LG>
+__device__ __forceinline__ float lanes_sum(float x) {
+#pragma unroll
     for (int o = LG >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
 
-// LG lanes hold one (row, group) at a time: lane l the vectors l, l + LG, ... of its D / V.  A lane
-// group keeps its group g over all of its rows, so the weights are read once.
-template <typename IO, int V, int K>
-__global__ void __launch_bounds__(kRowThreads) norm_rows_fwd_kernel(NormArgs p, int LG, int row_lanes) {
-    const int D = p.C / p.G, nv = D / V;
-    const int lane = threadIdx.x & (LG - 1);
-    const long long unit = ((long long)blockIdx.x * kRowThreads + threadIdx.x) / LG;
-    const int g = (int)(unit % p.G);
-    const long long first = unit / p.G;
-    float w[K][V], b[K][V];
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int v = lane + k * LG, c = g * D + v * V + i;
-            w[k][i] = p.weight && v < nv ? p.weight[c] : 1.f;
-            b[k][i] = p.bias && v < nv ? p.bias[c] : 0.f;
-        }
-    const float inv = 1.f / (float)D;
-    // the lane groups of one warp take the same number of steps, so that every shuffle has all lanes
-    for (long long r0 = 0; r0 < p.N; r0 += row_lanes) {
-        const long long row = r0 + first;
-        const bool live = first < row_lanes && row < p.N;
-        const long long base = row * p.C + (long long)g * D;
-        float x[K][V], gt[K][V];
-        float s = 0.f;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int v = lane + k * LG;
-            if (live && v < nv) {
-                load_vec<IO, V>(p.x, base + v * V, x[k]);
-                if (p.gate) load_vec<IO, V>(p.gate, base + v * V, gt[k]);
-#pragma unroll
-                for (int i = 0; i < V; ++i) s += x[k][i];
-            }
-        }
-        const float mean = lanes_sum(s, LG) * inv;
-        float q = 0.f;
+// What a lane of the rows form works on: LG lanes hold one (row, group) at a time, lane l the vectors l,
+// l + LG, ... of its D / V.  A lane group keeps its group g over all of its rows, so the weights are read
+// once.  Close to both bounds: memory, and the instructions of the activation and of the two
+// reductions.  The next row is requested before the current one is reduced, LG is a template
+// argument and the arithmetic runs on packed pairs (gated norm of 65536 x 16 heads of 128 at bf16: 365 us
+// without the three, 41 instructions an element).
+template <int V, int K, int LG>
+struct RowLane {
+    using U = Unit<V>;
+    int D, nv, lane, g, first;  // (row lanes are few: RowLane::first < the number of rows)
+    bool mine;
+    long long base, step;       // element of this lane's first vector, and to the next row's
+    U w[K][kUnits<V>], b[K][kUnits<V>];
+    __device__ RowLane(const NormArgs &p, int row_lanes) {
+        D = p.C / p.G;
+        nv = D / V;
+        lane = threadIdx.x & (LG - 1);
+        const int unit = (blockIdx.x * kRowThreads + threadIdx.x) / LG;
+        g = unit % p.G;
+        first = unit / p.G;
+        mine = first < row_lanes;
+        base = (long long)first * p.C + (long long)g * D + lane * V;
+        step = (long long)row_lanes * p.C;
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (live && lane + k * LG < nv)
 #pragma unroll
-                for (int i = 0; i < V; ++i) q = fmaf(x[k][i] - mean, x[k][i] - mean, q);
-        const float rstd = 1.f / sqrtf(fmaf(lanes_sum(q, LG), inv, p.eps));
+            for (int u = 0; u < kUnits<V>; ++u) {
+                const int c = g * D + (lane + k * LG) * V + 2 * u;
+                w[k][u] = channel_unit<V>(has(k) ? p.weight : nullptr, c, 1.f);
+                b[k][u] = channel_unit<V>(has(k) ? p.bias : nullptr, c, 0.f);
+            }
+    }
+    __device__ __forceinline__ bool has(int k) const { return lane + k * LG < nv; }
+};
+
+template <typename IO, int V, int K, int LG, int MODE>
+__global__ void __launch_bounds__(kRowThreads, K == 1 ? kRowFwdBlocks : 1) norm_rows_fwd_kernel(NormArgs p, int row_lanes) {
+    using U = Unit<V>;
+    constexpr int NU = kUnits<V>;
+    const RowLane<V, K, LG> t(p, row_lanes);
+    const float inv = 1.f / (float)t.D;
+    Pack<IO, V> xr[K], gr[K];
+    auto request = [&](int row, long long at) {
+        if (!t.mine || row >= p.N) return;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (t.has(k)) {
+                xr[k] = load_pack<IO, V>(p.x, at + k * LG * V);
+                if (mode_gate<MODE>(p)) gr[k] = load_pack<IO, V>(p.gate, at + k * LG * V);
+            }
+    };
+    long long at = t.base;
+    request(t.first, at);
+    // the lane groups of one warp take the same number of steps, so that every shuffle has all lanes
+    for (int r0 = 0; r0 < p.N; r0 += row_lanes, at += t.step) {
+        const int row = r0 + t.first;
+        const bool live = t.mine && row < p.N;
+        U x[K][NU], s = both<U>(0.f);
+        Pack<IO, V> gc[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            gc[k] = gr[k];
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+                x[k][u] = xr[k].unit(u);
+                if (t.has(k)) s = add(s, x[k][u]);
+            }
+        }
+        request(row + row_lanes, at + t.step);
+        const float mean = lanes_sum<LG>(total(s)) * inv;
+        U q = both<U>(0.f);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+                x[k][u] = add(x[k][u], both<U>(-mean));
+                if (t.has(k)) q = fma(x[k][u], x[k][u], q);
+            }
+        const float rstd = rsqrtf(fmaf(lanes_sum<LG>(total(q)), inv, p.eps));
         if (!live) continue;
-        if (lane == 0) {
-            if (p.mean) p.mean[row * p.G + g] = mean;
-            if (p.rstd) p.rstd[row * p.G + g] = rstd;
+        if (t.lane == 0) {
+            if (p.mean) p.mean[(long long)row * p.G + t.g] = mean;
+            if (p.rstd) p.rstd[(long long)row * p.G + t.g] = rstd;
         }
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int v = lane + k * LG;
-            if (v >= nv) continue;
-            float y[V];
+            if (!t.has(k)) continue;
+            Pack<IO, V> y;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float z = fmaf((x[k][i] - mean) * rstd, w[k][i], b[k][i]);
-                y[i] = p.gate ? z * act_value(p.act, gt[k][i]) : act_value(p.act, z);
-            }
-            store_vec<IO, V>(p.y, base + v * V, y);
+            for (int u = 0; u < NU; ++u)
+                y.set(u, y_of<IO, MODE>(p, fma(mul(x[k][u], both<U>(rstd)), t.w[k][u], t.b[k][u]), gc[k].unit(u)));
+            store_pack<IO, V>(p.y, at + k * LG * V, y);
         }
     }
 }
 
 // The same lanes for the backward pass; a lane also sums dz and dz xh of its channels over its rows.
-template <typename IO, int V, int K>
-__global__ void __launch_bounds__(kRowThreads) norm_rows_bwd_kernel(NormArgs p, int LG, int row_lanes) {
-    const int D = p.C / p.G, nv = D / V;
-    const int lane = threadIdx.x & (LG - 1);
-    const long long unit = ((long long)blockIdx.x * kRowThreads + threadIdx.x) / LG;
-    const int g = (int)(unit % p.G);
-    const long long first = unit / p.G;
-    float w[K][V], b[K][V], sz[K][V], szx[K][V];
+template <typename IO, int V, int K, int LG, int MODE>
+__global__ void __launch_bounds__(kRowThreads, K == 1 ? kRowBwdBlocks : 1) norm_rows_bwd_kernel(NormArgs p, int row_lanes) {
+    using U = Unit<V>;
+    constexpr int NU = kUnits<V>;
+    const RowLane<V, K, LG> t(p, row_lanes);
+    const float inv = 1.f / (float)t.D;
+    U sz[K][NU], szx[K][NU];
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int v = lane + k * LG, c = g * D + v * V + i;
-            w[k][i] = p.weight && v < nv ? p.weight[c] : 1.f;
-            b[k][i] = p.bias && v < nv ? p.bias[c] : 0.f;
-            sz[k][i] = szx[k][i] = 0.f;
-        }
-    const float inv = 1.f / (float)D;
-    for (long long r0 = 0; r0 < p.N; r0 += row_lanes) {
-        const long long row = r0 + first;
-        const bool live = first < row_lanes && row < p.N;
-        const long long base = row * p.C + (long long)g * D;
-        const float mean = live ? p.mean[row * p.G + g] : 0.f, rstd = live ? p.rstd[row * p.G + g] : 0.f;
-        float xh[K][V], dn[K][V];
-        float s1 = 0.f, s2 = 0.f;
+        for (int u = 0; u < NU; ++u) sz[k][u] = szx[k][u] = both<U>(0.f);
+    Pack<IO, V> xr[K], dr[K], gr[K];
+    float mean_n = 0.f, rstd_n = 0.f;
+    auto request = [&](int row, long long at) {
+        if (!t.mine || row >= p.N) return;
+        mean_n = p.mean[(long long)row * p.G + t.g];
+        rstd_n = p.rstd[(long long)row * p.G + t.g];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (t.has(k)) {
+                xr[k] = load_pack<IO, V>(p.x, at + k * LG * V);
+                dr[k] = load_pack<IO, V>(p.dy, at + k * LG * V);
+                if (mode_gate<MODE>(p)) gr[k] = load_pack<IO, V>(p.gate, at + k * LG * V);
+            }
+    };
+    long long at = t.base;
+    request(t.first, at);
+    for (int r0 = 0; r0 < p.N; r0 += row_lanes, at += t.step) {
+        const int row = r0 + t.first;
+        const bool live = t.mine && row < p.N;
+        const float mean = mean_n, rstd = rstd_n;
+        U xh[K][NU], dn[K][NU], s1 = both<U>(0.f), s2 = both<U>(0.f);
+        Pack<IO, V> dg[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int v = lane + k * LG;
-            if (!live || v >= nv) continue;
-            float x[V], dy[V], gt[V] = {}, dg[V];
-            load_vec<IO, V>(p.x, base + v * V, x);
-            load_vec<IO, V>(p.dy, base + v * V, dy);
-            if (p.gate) load_vec<IO, V>(p.gate, base + v * V, gt);
+            if (!live || !t.has(k)) continue;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                xh[k][i] = (x[i] - mean) * rstd;
-                const float dz = dz_of(p, fmaf(xh[k][i], w[k][i], b[k][i]), dy[i], gt[i], dg[i]);
-                sz[k][i] += dz;
-                szx[k][i] = fmaf(dz, xh[k][i], szx[k][i]);
-                dn[k][i] = dz * w[k][i];
-                s1 += dn[k][i];
-                s2 = fmaf(dn[k][i], xh[k][i], s2);
+            for (int u = 0; u < NU; ++u) {
+                xh[k][u] = mul(add(xr[k].unit(u), both<U>(-mean)), both<U>(rstd));
+                U d;
+                const U dz = dz_of<IO, MODE>(p, fma(xh[k][u], t.w[k][u], t.b[k][u]), dr[k].unit(u), gr[k].unit(u), d);
+                dg[k].set(u, d);
+                sz[k][u] = add(sz[k][u], dz);
+                szx[k][u] = fma(dz, xh[k][u], szx[k][u]);
+                dn[k][u] = mul(dz, t.w[k][u]);
+                s1 = add(s1, dn[k][u]);
+                s2 = fma(dn[k][u], xh[k][u], s2);
             }
-            if (p.gate) store_vec<IO, V>(p.dgate, base + v * V, dg);
+            if (mode_gate<MODE>(p)) store_pack<IO, V>(p.dgate, at + k * LG * V, dg[k]);
         }
-        s1 = lanes_sum(s1, LG) * inv;
-        s2 = lanes_sum(s2, LG) * inv;
+        request(row + row_lanes, at + t.step);
+        const float m1 = lanes_sum<LG>(total(s1)) * inv, m2 = lanes_sum<LG>(total(s2)) * inv;
         if (!live) continue;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int v = lane + k * LG;
-            if (v >= nv) continue;
-            float dx[V];
+            if (!t.has(k)) continue;
+            Pack<IO, V> dx;
 #pragma unroll
-            for (int i = 0; i < V; ++i) dx[i] = rstd * (dn[k][i] - s1 - xh[k][i] * s2);
-            store_vec<IO, V>(p.dx, base + v * V, dx);
+            for (int u = 0; u < NU; ++u)
+                dx.set(u, mul(both<U>(rstd), fma(xh[k][u], both<U>(-m2), add(dn[k][u], both<U>(-m1)))));
+            store_pack<IO, V>(p.dx, at + k * LG * V, dx);
         }
     }
-    if (!p.chan_parts || first >= row_lanes) return;
-    float *out = p.chan_parts + first * 2 * p.C + g * D;
+    if (!p.chan_parts || !t.mine) return;
+    float *out = p.chan_parts + (long long)t.first * 2 * p.C + t.g * t.D + t.lane * V;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int v = lane + k * LG;
-        if (v >= nv) continue;
+        if (!t.has(k)) continue;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            out[v * V + i] = sz[k][i];
-            out[p.C + v * V + i] = szx[k][i];
+        for (int u = 0; u < NU; ++u) {
+            float *o = out + k * LG * V + 2 * u;
+            if constexpr (V == 1) {
+                o[0] = sz[k][u];
+                o[p.C] = szx[k][u];
+            } else {
+                o[0] = first(sz[k][u]);
+                o[1] = second(sz[k][u]);
+                o[p.C] = first(szx[k][u]);
+                o[p.C + 1] = second(szx[k][u]);
+            }
         }
     }
 }
 
-// dbias, dweight: the parts' sums, a column per thread of x and 8 interleaved ranges of parts.
-__global__ void __launch_bounds__(256) norm_channel_sum_kernel(const float *parts, int n, int C, float *dweight, float *dbias) {
-    __shared__ float s[8][33];
-    const int col = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;  // col over [dz | dz xh]
-    float acc = 0.f;
+// dbias, dweight: the parts' sums, 32 columns of [dz | dz xh] per block and 32 interleaved ranges of parts,
+// four loads in flight per thread.
+__global__ void __launch_bounds__(1024) norm_channel_sum_kernel(const float *parts, int n, int C, float *dweight, float *dbias) {
+    __shared__ float s[32][33];
+    const int lane = threadIdx.x & 31, k = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+    float acc[4] = {};
     if (col < 2 * C)
-        for (int i = k; i < n; i += 8) acc += parts[(long long)i * 2 * C + col];
-    s[k][threadIdx.x & 31] = acc;
+        for (int i = k; i < n; i += 128)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i + 32 * u < n) acc[u] += parts[(long long)(i + 32 * u) * 2 * C + col];
+    s[k][lane] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
     __syncthreads();
-    if (k == 0 && col < 2 * C) {
-        for (int i = 1; i < 8; ++i) acc += s[i][threadIdx.x];
-        if (col < C) {
-            if (dbias) dbias[col] = acc;
+    const float sum = warp_sum(s[lane][k]);  // warp k: column k of the block
+    const int c = blockIdx.x * 32 + k;
+    if (lane == 0 && c < 2 * C) {
+        if (c < C) {
+            if (dbias) dbias[c] = sum;
         } else if (dweight) {
-            dweight[col - C] = acc;
+            dweight[c - C] = sum;
         }
     }
 }
 
 // ---- tiles form ----------------------------------------------------------------------------------
 
-constexpr int kTileThreads = 512;
+constexpr int kTileThreads = 256;
 constexpr int kTileCols = 256;  // vector columns of a block
+constexpr int kTileAhead = 4, kGradAhead = 2;  // positions that a thread requests at a time
 
 struct Stat {
     float n, mean, m2;
@@ -270,7 +423,7 @@ struct Stat {
 __device__ __forceinline__ Stat merge(const Stat &a, const Stat &b) {
     const float n = a.n + b.n;
     if (n == 0.f) return a;
-    const float f = b.n / n, d = b.mean - a.mean;
+    const float f = __fdividef(b.n, n), d = b.mean - a.mean;
     return Stat{n, fmaf(d, f, a.mean), a.m2 + b.m2 + d * d * a.n * f};
 }
 __device__ __forceinline__ Stat shfl(const Stat &a, int o) {
@@ -283,9 +436,9 @@ template <int V>
 struct Tile {
     int n, tile, cb, c0, c1, cols, RL, col, rl, s0, s1;
     bool live;
-    __device__ explicit Tile(const NormArgs &p) {
-        n = blockIdx.x / p.tiles;
-        tile = blockIdx.x % p.tiles;
+    __device__ Tile(const NormArgs &p, int unit) {  // unit: n * tiles + tile
+        n = unit / p.tiles;
+        tile = unit % p.tiles;
         cb = blockIdx.y;
         c0 = cb * kTileCols * V;
         c1 = min(c0 + kTileCols * V, p.C);
@@ -306,23 +459,29 @@ struct Tile {
 __host__ __device__ inline int norm_pieces(int G, int blocks) { return G + blocks - 1; }
 
 template <typename IO, int V>
-__global__ void __launch_bounds__(kTileThreads) norm_tile_stats_kernel(NormArgs p) {
+__global__ void __launch_bounds__(kTileThreads, 2) norm_tile_stats_kernel(NormArgs p) {
     __shared__ float sh_mean[kTileThreads * V], sh_m2[kTileThreads * V];
-    const Tile<V> t(p);
+    const Tile<V> t(p, blockIdx.x);
     const int D = p.C / p.G;
     float mean[V] = {}, m2[V] = {};
     float cnt = 0.f;
     if (t.live)
-        for (int s = t.s0 + t.rl; s < t.s1; s += t.RL) {
-            float x[V];
-            load_vec<IO, V>(p.x, t.at(p, s), x);
-            cnt += 1.f;
-            const float f = 1.f / cnt;
+        for (int s = t.s0 + t.rl; s < t.s1; s += kTileAhead * t.RL) {
+            Pack<IO, V> x[kTileAhead];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float d = x[i] - mean[i];
-                mean[i] = fmaf(d, f, mean[i]);
-                m2[i] = fmaf(d, x[i] - mean[i], m2[i]);
+            for (int u = 0; u < kTileAhead; ++u)
+                if (s + u * t.RL < t.s1) x[u] = load_pack<IO, V>(p.x, t.at(p, s + u * t.RL));
+#pragma unroll
+            for (int u = 0; u < kTileAhead; ++u) {
+                if (s + u * t.RL >= t.s1) break;
+                cnt += 1.f;
+                const float f = __fdividef(1.f, cnt);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float d = x[u].at(i) - mean[i];
+                    mean[i] = fmaf(d, f, mean[i]);
+                    m2[i] = fmaf(d, x[u].at(i) - mean[i], m2[i]);
+                }
             }
         }
     const int width = t.c1 - t.c0;
@@ -370,15 +529,15 @@ __device__ __forceinline__ Stat merge_pieces(const NormArgs &p, int n, int g, in
     return st;
 }
 
-template <typename IO, int V>
-__global__ void __launch_bounds__(kTileThreads) norm_tile_apply_kernel(NormArgs p) {
+template <typename IO, int V, int MODE>
+__global__ void __launch_bounds__(kTileThreads, 2) norm_tile_apply_kernel(NormArgs p) {
     __shared__ float sh_mean[kTileCols * V], sh_rstd[kTileCols * V];
-    const Tile<V> t(p);
+    const Tile<V> t(p, blockIdx.x);
     const int D = p.C / p.G, g0 = t.first_group(D);
     for (int g = g0 + (threadIdx.x >> 5); g <= t.last_group(D); g += kTileThreads / 32) {
         const Stat st = merge_pieces<V>(p, t.n, g, gridDim.y);
         if ((threadIdx.x & 31) == 0) {
-            const float rstd = 1.f / sqrtf(st.m2 / ((float)D * (float)p.S) + p.eps);
+            const float rstd = rsqrtf(st.m2 / ((float)D * (float)p.S) + p.eps);
             sh_mean[g - g0] = st.mean;
             sh_rstd[g - g0] = rstd;
             if (t.tile == 0 && g * D >= t.c0) {  // the block with the group's first channel
@@ -398,94 +557,121 @@ __global__ void __launch_bounds__(kTileThreads) norm_tile_apply_kernel(NormArgs 
         w[i] = p.weight ? p.weight[c] : 1.f;
         b[i] = p.bias ? p.bias[c] : 0.f;
     }
-    for (int s = t.s0 + t.rl; s < t.s1; s += t.RL) {
-        const long long at = t.at(p, s);
-        float x[V], gt[V] = {}, y[V];
-        load_vec<IO, V>(p.x, at, x);
-        if (p.gate) load_vec<IO, V>(p.gate, at, gt);
+    for (int s = t.s0 + t.rl; s < t.s1; s += kTileAhead * t.RL) {
+        Pack<IO, V> x[kTileAhead], gt[kTileAhead];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float z = fmaf((x[i] - mean[i]) * rstd[i], w[i], b[i]);
-            y[i] = p.gate ? z * act_value(p.act, gt[i]) : act_value(p.act, z);
+        for (int u = 0; u < kTileAhead; ++u)
+            if (s + u * t.RL < t.s1) {
+                x[u] = load_pack<IO, V>(p.x, t.at(p, s + u * t.RL));
+                if (mode_gate<MODE>(p)) gt[u] = load_pack<IO, V>(p.gate, t.at(p, s + u * t.RL));
+            }
+#pragma unroll
+        for (int u = 0; u < kTileAhead; ++u) {
+            if (s + u * t.RL >= t.s1) break;
+            Pack<IO, V> y;
+#pragma unroll
+            for (int i = 0; i < V; ++i) st_io(y.v, i, y_of<IO, MODE>(p, fmaf((x[u].at(i) - mean[i]) * rstd[i], w[i], b[i]), gt[u].at(i)));
+            store_pack<IO, V>(p.y, t.at(p, s + u * t.RL), y);
         }
-        store_vec<IO, V>(p.y, at, y);
     }
 }
 
 // First kernel of the backward pass: per channel sum dz and sum dz xh over the tile, and their sums over
-// each group piece with the weights.
-template <typename IO, int V>
-__global__ void __launch_bounds__(kTileThreads) norm_tile_grad_sums_kernel(NormArgs p) {
+// each group piece with the weights.  A block takes every gridDim.x-th tile of all samples and keeps its
+// channels' totals, so that the parts of dweight and dbias stay few.
+template <typename IO, int V, int MODE>
+__global__ void __launch_bounds__(kTileThreads, 2) norm_tile_grad_sums_kernel(NormArgs p) {
     __shared__ float sh1[kTileThreads * V], sh2[kTileThreads * V];
-    const Tile<V> t(p);
-    const int D = p.C / p.G, width = t.c1 - t.c0;
-    if (t.live) {
-        float mean[V], rstd[V], w[V], b[V], sz[V] = {}, szx[V] = {};
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = t.c0 + t.col * V + i;
-            mean[i] = p.mean[(long long)t.n * p.G + c / D];
-            rstd[i] = p.rstd[(long long)t.n * p.G + c / D];
-            w[i] = p.weight ? p.weight[c] : 1.f;
-            b[i] = p.bias ? p.bias[c] : 0.f;
-        }
-        for (int s = t.s0 + t.rl; s < t.s1; s += t.RL) {
-            const long long at = t.at(p, s);
-            float x[V], dy[V], gt[V] = {}, dg;
-            load_vec<IO, V>(p.x, at, x);
-            load_vec<IO, V>(p.dy, at, dy);
-            if (p.gate) load_vec<IO, V>(p.gate, at, gt);
+    __shared__ float tot1[kTileCols * V], tot2[kTileCols * V];
+    const int D = p.C / p.G;
+    for (int i = threadIdx.x; i < kTileCols * V; i += kTileThreads) tot1[i] = tot2[i] = 0.f;
+    for (int unit = blockIdx.x; unit < p.N * p.tiles; unit += gridDim.x) {
+        const Tile<V> t(p, unit);
+        const int width = t.c1 - t.c0;
+        __syncthreads();
+        if (t.live) {
+            float mean[V], rstd[V], w[V], b[V], sz[V] = {}, szx[V] = {};
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float xh = (x[i] - mean[i]) * rstd[i];
-                const float dz = dz_of(p, fmaf(xh, w[i], b[i]), dy[i], gt[i], dg);
-                sz[i] += dz;
-                szx[i] = fmaf(dz, xh, szx[i]);
+                const int c = t.c0 + t.col * V + i;
+                mean[i] = p.mean[(long long)t.n * p.G + c / D];
+                rstd[i] = p.rstd[(long long)t.n * p.G + c / D];
+                w[i] = p.weight ? p.weight[c] : 1.f;
+                b[i] = p.bias ? p.bias[c] : 0.f;
+            }
+            for (int s = t.s0 + t.rl; s < t.s1; s += kGradAhead * t.RL) {
+                Pack<IO, V> x[kGradAhead], dy[kGradAhead], gt[kGradAhead];
+#pragma unroll
+                for (int u = 0; u < kGradAhead; ++u)
+                    if (s + u * t.RL < t.s1) {
+                        const long long at = t.at(p, s + u * t.RL);
+                        x[u] = load_pack<IO, V>(p.x, at);
+                        dy[u] = load_pack<IO, V>(p.dy, at);
+                        if (mode_gate<MODE>(p)) gt[u] = load_pack<IO, V>(p.gate, at);
+                    }
+#pragma unroll
+                for (int u = 0; u < kGradAhead; ++u) {
+                    if (s + u * t.RL >= t.s1) break;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float xh = (x[u].at(i) - mean[i]) * rstd[i];
+                        float dg;
+                        const float dz = dz_of<IO, MODE>(p, fmaf(xh, w[i], b[i]), dy[u].at(i), gt[u].at(i), dg);
+                        sz[i] += dz;
+                        szx[i] = fmaf(dz, xh, szx[i]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                sh1[t.rl * width + t.col * V + i] = sz[i];
+                sh2[t.rl * width + t.col * V + i] = szx[i];
             }
         }
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            sh1[t.rl * width + t.col * V + i] = sz[i];
-            sh2[t.rl * width + t.col * V + i] = szx[i];
+        __syncthreads();
+        for (int c = threadIdx.x; c < width; c += kTileThreads) {
+            float a = 0.f, b = 0.f;
+            for (int r = 0; r < t.RL; ++r) {
+                a += sh1[r * width + c];
+                b += sh2[r * width + c];
+            }
+            tot1[c] += a;
+            tot2[c] += b;
+            const float w = p.weight ? p.weight[t.c0 + c] : 1.f;
+            sh1[c] = a * w;  // row lane 0's place, which only this thread reads
+            sh2[c] = b * w;
+        }
+        __syncthreads();
+        const int lane = threadIdx.x & 31;
+        for (int g = t.first_group(D) + (threadIdx.x >> 5); g <= t.last_group(D); g += kTileThreads / 32) {
+            const int a = max(g * D, t.c0) - t.c0, b = min((g + 1) * D, t.c1) - t.c0;
+            float s1 = 0.f, s2 = 0.f;
+            for (int c = a + lane; c < b; c += 32) {
+                s1 += sh1[c];
+                s2 += sh2[c];
+            }
+            s1 = warp_sum(s1);
+            s2 = warp_sum(s2);
+            if (lane == 0) {
+                float *out = p.stat_parts + 2 * ((long long)unit * norm_pieces(p.G, gridDim.y) + g + t.cb);
+                out[0] = s1;
+                out[1] = s2;
+            }
         }
     }
-    __syncthreads();
-    float *chan = p.chan_parts + (long long)blockIdx.x * 2 * p.C + t.c0;
-    for (int c = threadIdx.x; c < width; c += kTileThreads) {
-        float a = 0.f, b = 0.f;
-        for (int r = 0; r < t.RL; ++r) {
-            a += sh1[r * width + c];
-            b += sh2[r * width + c];
-        }
-        chan[c] = a;
-        chan[p.C + c] = b;
-        const float w = p.weight ? p.weight[t.c0 + c] : 1.f;
-        sh1[c] = a * w;  // row lane 0's place, which only this thread reads
-        sh2[c] = b * w;
-    }
-    __syncthreads();
-    const int lane = threadIdx.x & 31;
-    for (int g = t.first_group(D) + (threadIdx.x >> 5); g <= t.last_group(D); g += kTileThreads / 32) {
-        const int a = max(g * D, t.c0) - t.c0, b = min((g + 1) * D, t.c1) - t.c0;
-        float s1 = 0.f, s2 = 0.f;
-        for (int c = a + lane; c < b; c += 32) {
-            s1 += sh1[c];
-            s2 += sh2[c];
-        }
-        s1 = warp_sum(s1);
-        s2 = warp_sum(s2);
-        if (lane == 0) {
-            float *out = p.stat_parts + 2 * (((long long)blockIdx.x) * norm_pieces(p.G, gridDim.y) + g + t.cb);
-            out[0] = s1;
-            out[1] = s2;
-        }
+    if (!p.chan_parts) return;
+    const int c0 = blockIdx.y * kTileCols * V, width = min(kTileCols * V, p.C - c0);
+    float *chan = p.chan_parts + (long long)blockIdx.x * 2 * p.C + c0;
+    for (int c = threadIdx.x; c < width; c += kTileThreads) {  // each thread its own totals
+        chan[c] = tot1[c];
+        chan[p.C + c] = tot2[c];
     }
 }
 
-template <typename IO, int V>
-__global__ void __launch_bounds__(kTileThreads) norm_tile_grad_apply_kernel(NormArgs p) {
+template <typename IO, int V, int MODE>
+__global__ void __launch_bounds__(kTileThreads, 2) norm_tile_grad_apply_kernel(NormArgs p) {
     __shared__ float sh1[kTileCols * V], sh2[kTileCols * V];
-    const Tile<V> t(p);
+    const Tile<V> t(p, blockIdx.x);
     const int D = p.C / p.G, g0 = t.first_group(D), lane = threadIdx.x & 31;
     const float inv = 1.f / ((float)D * (float)p.S);
     for (int g = g0 + (threadIdx.x >> 5); g <= t.last_group(D); g += kTileThreads / 32) {
@@ -516,20 +702,32 @@ __global__ void __launch_bounds__(kTileThreads) norm_tile_grad_apply_kernel(Norm
         s1[i] = sh1[g - g0];
         s2[i] = sh2[g - g0];
     }
-    for (int s = t.s0 + t.rl; s < t.s1; s += t.RL) {
-        const long long at = t.at(p, s);
-        float x[V], dy[V], gt[V] = {}, dg[V], dx[V];
-        load_vec<IO, V>(p.x, at, x);
-        load_vec<IO, V>(p.dy, at, dy);
-        if (p.gate) load_vec<IO, V>(p.gate, at, gt);
+    for (int s = t.s0 + t.rl; s < t.s1; s += kGradAhead * t.RL) {
+        Pack<IO, V> x[kGradAhead], dy[kGradAhead], gt[kGradAhead];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float xh = (x[i] - mean[i]) * rstd[i];
-            const float dz = dz_of(p, fmaf(xh, w[i], b[i]), dy[i], gt[i], dg[i]);
-            dx[i] = rstd[i] * (fmaf(dz, w[i], -s1[i]) - xh * s2[i]);
+        for (int u = 0; u < kGradAhead; ++u)
+            if (s + u * t.RL < t.s1) {
+                const long long at = t.at(p, s + u * t.RL);
+                x[u] = load_pack<IO, V>(p.x, at);
+                dy[u] = load_pack<IO, V>(p.dy, at);
+                if (mode_gate<MODE>(p)) gt[u] = load_pack<IO, V>(p.gate, at);
+            }
+#pragma unroll
+        for (int u = 0; u < kGradAhead; ++u) {
+            if (s + u * t.RL >= t.s1) break;
+            const long long at = t.at(p, s + u * t.RL);
+            Pack<IO, V> dgv, dxv;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float xh = (x[u].at(i) - mean[i]) * rstd[i];
+                float dg;
+                const float dz = dz_of<IO, MODE>(p, fmaf(xh, w[i], b[i]), dy[u].at(i), gt[u].at(i), dg);
+                st_io(dxv.v, i, rstd[i] * (fmaf(dz, w[i], -s1[i]) - xh * s2[i]));
+                st_io(dgv.v, i, dg);
+            }
+            store_pack<IO, V>(p.dx, at, dxv);
+            if (mode_gate<MODE>(p)) store_pack<IO, V>(p.dgate, at, dgv);
         }
-        store_vec<IO, V>(p.dx, at, dx);
-        if (p.gate) store_vec<IO, V>(p.dgate, at, dg);
     }
 }
 
@@ -551,11 +749,11 @@ NormPlan plan_of(const prism_norm_shape &s, bool backward) {
     pl.rows = s.S == 1 && nv <= 32 * kRowVecs;
     const int sms = sm_count();
     if (pl.rows) {
-        pl.LG = 1;
+        pl.LG = 4;
         while (pl.LG < nv && pl.LG < 32) pl.LG *= 2;
-        pl.K = nv <= 32 ? 1 : kRowVecs;
+        pl.K = nv <= 32 && pl.V > 1 ? 1 : kRowVecs;
         const long long per_block = kRowThreads / pl.LG;
-        long long lanes = std::max<long long>(1, (long long)sms * (backward ? 4 : 8) * per_block / s.G);
+        long long lanes = std::max<long long>(1, (long long)sms * (pl.K > 1 ? 1 : backward ? kRowBwdBlocks : kRowFwdBlocks) * per_block / s.G);
         lanes = std::min<long long>(lanes, std::max(1, s.N));
         pl.row_lanes = (int)lanes;
         pl.blocks = (int)((lanes * s.G + per_block - 1) / per_block);
@@ -564,7 +762,7 @@ NormPlan plan_of(const prism_norm_shape &s, bool backward) {
     pl.V = s.C % full == 0 ? full : 1;
     pl.col_blocks = (s.C / pl.V + kTileCols - 1) / kTileCols;
     const long long others = std::max(1LL, (long long)s.N * pl.col_blocks);
-    pl.tiles = (int)std::max<long long>(1, std::min<long long>((4LL * sms + others - 1) / others, s.S / 16));
+    pl.tiles = (int)std::max<long long>(1, std::min<long long>((2LL * sms + others - 1) / others, s.S / 16));
     return pl;
 }
 
@@ -572,7 +770,9 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 size_t stat_bytes(const prism_norm_shape &s, const NormPlan &pl) {
     return pl.rows ? 0 : align256((size_t)s.N * pl.tiles * norm_pieces(s.G, pl.col_blocks) * 8);
 }
-int chan_parts(const prism_norm_shape &s, const NormPlan &pl) { return pl.rows ? pl.row_lanes : s.N * pl.tiles; }
+int chan_parts(const prism_norm_shape &s, const NormPlan &pl) {
+    return pl.rows ? pl.row_lanes : (int)std::min<long long>((long long)s.N * pl.tiles, 2LL * sm_count());
+}
 
 prism_status check_shape(const prism_norm_shape *s) {
     if (!s) return PRISM_ERR_INVALID_ARG;
@@ -584,20 +784,47 @@ prism_status check_shape(const prism_norm_shape *s) {
     return PRISM_OK;
 }
 
+// f(mode) with the call's activation and gate as a compile-time mode.
+template <typename F>
+void with_mode(const NormArgs &a, F f) {
+    const bool g = a.gate != nullptr;
+    switch (a.act) {
+        case PRISM_ACT_SILU: g ? f(std::integral_constant<int, 3>()) : f(std::integral_constant<int, 2>()); break;
+        case PRISM_ACT_GELU: g ? f(std::integral_constant<int, 5>()) : f(std::integral_constant<int, 4>()); break;
+        default: g ? f(std::integral_constant<int, 1>()) : f(std::integral_constant<int, 0>()); break;
+    }
+}
+
+// f(lanes) with the plan's lanes of a group as a compile-time number.
+template <typename F>
+void with_lanes(int LG, F f) {
+    switch (LG) {
+        case 4: f(std::integral_constant<int, 4>()); break;
+        case 8: f(std::integral_constant<int, 8>()); break;
+        case 16: f(std::integral_constant<int, 16>()); break;
+        default: f(std::integral_constant<int, 32>()); break;
+    }
+}
+
 template <typename IO>
 cudaError_t launch_fwd(const NormArgs &a, const NormPlan &pl, cudaStream_t s) {
     constexpr int F = 16 / sizeof(IO);
     launch_probe_mark(s);
     if (pl.rows) {
-        auto kern = pl.V == 1 ? (pl.K == 1 ? norm_rows_fwd_kernel<IO, 1, 1> : norm_rows_fwd_kernel<IO, 1, kRowVecs>)
-                              : (pl.K == 1 ? norm_rows_fwd_kernel<IO, F, 1> : norm_rows_fwd_kernel<IO, F, kRowVecs>);
-        kern<<<pl.blocks, kRowThreads, 0, s>>>(a, pl.LG, pl.row_lanes);
+        with_lanes(pl.LG, [&](auto l) {
+            if (pl.V == 1) norm_rows_fwd_kernel<IO, 1, kRowVecs, l.value, kRuntime><<<pl.blocks, kRowThreads, 0, s>>>(a, pl.row_lanes);
+            else if (pl.K == 1)
+                with_mode(a, [&](auto m) { norm_rows_fwd_kernel<IO, F, 1, l.value, m.value><<<pl.blocks, kRowThreads, 0, s>>>(a, pl.row_lanes); });
+            else if constexpr (l.value == 32)  // (several vectors of a lane only where 32 lanes are too few)
+                norm_rows_fwd_kernel<IO, F, kRowVecs, 32, kRuntime><<<pl.blocks, kRowThreads, 0, s>>>(a, pl.row_lanes);
+        });
         return cudaGetLastError();
     }
     const dim3 grid(a.N * a.tiles, pl.col_blocks);
     (pl.V == 1 ? norm_tile_stats_kernel<IO, 1> : norm_tile_stats_kernel<IO, F>)<<<grid, kTileThreads, 0, s>>>(a);
     launch_probe_mark(s);
-    (pl.V == 1 ? norm_tile_apply_kernel<IO, 1> : norm_tile_apply_kernel<IO, F>)<<<grid, kTileThreads, 0, s>>>(a);
+    if (pl.V == 1) norm_tile_apply_kernel<IO, 1, kRuntime><<<grid, kTileThreads, 0, s>>>(a);
+    else with_mode(a, [&](auto m) { norm_tile_apply_kernel<IO, F, m.value><<<grid, kTileThreads, 0, s>>>(a); });
     return cudaGetLastError();
 }
 
@@ -606,18 +833,24 @@ cudaError_t launch_bwd(const NormArgs &a, const NormPlan &pl, float *dweight, fl
     constexpr int F = 16 / sizeof(IO);
     launch_probe_mark(s);
     if (pl.rows) {
-        auto kern = pl.V == 1 ? (pl.K == 1 ? norm_rows_bwd_kernel<IO, 1, 1> : norm_rows_bwd_kernel<IO, 1, kRowVecs>)
-                              : (pl.K == 1 ? norm_rows_bwd_kernel<IO, F, 1> : norm_rows_bwd_kernel<IO, F, kRowVecs>);
-        kern<<<pl.blocks, kRowThreads, 0, s>>>(a, pl.LG, pl.row_lanes);
+        with_lanes(pl.LG, [&](auto l) {
+            if (pl.V == 1) norm_rows_bwd_kernel<IO, 1, kRowVecs, l.value, kRuntime><<<pl.blocks, kRowThreads, 0, s>>>(a, pl.row_lanes);
+            else if (pl.K == 1)
+                with_mode(a, [&](auto m) { norm_rows_bwd_kernel<IO, F, 1, l.value, m.value><<<pl.blocks, kRowThreads, 0, s>>>(a, pl.row_lanes); });
+            else if constexpr (l.value == 32)  // (several vectors of a lane only where 32 lanes are too few)
+                norm_rows_bwd_kernel<IO, F, kRowVecs, 32, kRuntime><<<pl.blocks, kRowThreads, 0, s>>>(a, pl.row_lanes);
+        });
     } else {
         const dim3 grid(a.N * a.tiles, pl.col_blocks);
-        (pl.V == 1 ? norm_tile_grad_sums_kernel<IO, 1> : norm_tile_grad_sums_kernel<IO, F>)<<<grid, kTileThreads, 0, s>>>(a);
+        if (pl.V == 1) norm_tile_grad_sums_kernel<IO, 1, kRuntime><<<dim3(a.parts, pl.col_blocks), kTileThreads, 0, s>>>(a);
+        else with_mode(a, [&](auto m) { norm_tile_grad_sums_kernel<IO, F, m.value><<<dim3(a.parts, pl.col_blocks), kTileThreads, 0, s>>>(a); });
         launch_probe_mark(s);
-        (pl.V == 1 ? norm_tile_grad_apply_kernel<IO, 1> : norm_tile_grad_apply_kernel<IO, F>)<<<grid, kTileThreads, 0, s>>>(a);
+        if (pl.V == 1) norm_tile_grad_apply_kernel<IO, 1, kRuntime><<<grid, kTileThreads, 0, s>>>(a);
+        else with_mode(a, [&](auto m) { norm_tile_grad_apply_kernel<IO, F, m.value><<<grid, kTileThreads, 0, s>>>(a); });
     }
     if (dweight || dbias) {
         launch_probe_mark(s);
-        norm_channel_sum_kernel<<<(2 * a.C + 31) / 32, 256, 0, s>>>(a.chan_parts, a.parts, a.C, dweight, dbias);
+        norm_channel_sum_kernel<<<(2 * a.C + 31) / 32, 1024, 0, s>>>(a.chan_parts, a.parts, a.C, dweight, dbias);
     }
     return cudaGetLastError();
 }
@@ -712,7 +945,7 @@ prism_status prism_group_norm_bwd(const prism_norm_shape *shape, const void *x, 
     a.stat_parts = (float *)workspace;
     a.chan_parts = (float *)((char *)workspace + stat_bytes(s, pl));
     a.parts = chan_parts(s, pl);
-    if (pl.rows && !dweight && !dbias) a.chan_parts = nullptr;
+    if (!dweight && !dbias) a.chan_parts = nullptr;
     const cudaError_t err = s.io == PRISM_F32 ? launch_bwd<float>(a, pl, dweight, dbias, (cudaStream_t)stream)
                                               : launch_bwd<__nv_bfloat16>(a, pl, dweight, dbias, (cudaStream_t)stream);
     probe_finish((cudaStream_t)stream);
