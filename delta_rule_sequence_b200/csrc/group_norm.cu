@@ -241,30 +241,68 @@ struct RowLane {
     __device__ __forceinline__ bool has(int k) const { return lane + k * LG < nv; }
 };
 
+// A thread's own vectors of the rows to come, NT tensors, kRing - 1 rows ahead: asynchronous copies into
+// shared memory (read back by the same thread, so there is nothing to synchronise).  Registers for one row
+// ahead kept 32 KB in flight per SM, 4.5 TB/s.
+constexpr int kRing = 4;
+
+template <typename IO, int V, int NT>
+struct RowRing {
+    static_assert(sizeof(Pack<IO, V>) == 16, "16-byte copies");
+    Pack<IO, V> (*buf)[NT][kRowThreads];  // [kRing], shared
+    __device__ __forceinline__ void copy(int slot, int tensor, const void *p, long long at) const {
+        const uint32_t dst = (uint32_t)__cvta_generic_to_shared(&buf[slot][tensor][threadIdx.x]);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"((const IO *)p + at) : "memory");
+    }
+    __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    // every copy but those of the kRing - 1 latest rows has landed
+    __device__ __forceinline__ static void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory"); }
+    __device__ __forceinline__ Pack<IO, V> get(int slot, int tensor) const { return buf[slot][tensor][threadIdx.x]; }
+};
+
 template <typename IO, int V, int K, int LG, int MODE>
 __global__ void __launch_bounds__(kRowThreads, K == 1 ? kRowFwdBlocks : 1) norm_rows_fwd_kernel(NormArgs p, int row_lanes) {
     using U = Unit<V>;
     constexpr int NU = kUnits<V>;
+    constexpr bool RING = K == 1 && V > 1;
+    __shared__ Pack<IO, V> buf[RING ? kRing : 1][2][RING ? kRowThreads : 1];
     const RowLane<V, K, LG> t(p, row_lanes);
     const float inv = 1.f / (float)t.D;
     Pack<IO, V> xr[K], gr[K];
-    auto request = [&](int row, long long at) {
-        if (!t.mine || row >= p.N) return;
+    int slot = 0;
+    auto request = [&](int row, long long at, int to) {  // into ring slot `to`, or registers
+        if (t.mine && row < p.N)
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (t.has(k)) {
-                xr[k] = load_pack<IO, V>(p.x, at + k * LG * V);
-                if (mode_gate<MODE>(p)) gr[k] = load_pack<IO, V>(p.gate, at + k * LG * V);
-            }
+            for (int k = 0; k < K; ++k)
+                if (t.has(k)) {
+                    if constexpr (RING) {
+                        const RowRing<IO, V, 2> ring{buf};
+                        ring.copy(to, 0, p.x, at);
+                        if (mode_gate<MODE>(p)) ring.copy(to, 1, p.gate, at);
+                    } else {
+                        xr[k] = load_pack<IO, V>(p.x, at + k * LG * V);
+                        if (mode_gate<MODE>(p)) gr[k] = load_pack<IO, V>(p.gate, at + k * LG * V);
+                    }
+                }
+        if constexpr (RING) RowRing<IO, V, 2>::commit();
     };
     long long at = t.base;
-    request(t.first, at);
+#pragma unroll
+    for (int k = 0; k < (RING ? kRing - 1 : 1); ++k) request(t.first + k * row_lanes, at + k * t.step, k);
     // the lane groups of one warp take the same number of steps, so that every shuffle has all lanes
     for (int r0 = 0; r0 < p.N; r0 += row_lanes, at += t.step) {
         const int row = r0 + t.first;
         const bool live = t.mine && row < p.N;
         U x[K][NU], s = both<U>(0.f);
         Pack<IO, V> gc[K];
+        if constexpr (RING) {
+            request(row + (kRing - 1) * row_lanes, at + (kRing - 1) * t.step, (slot + kRing - 1) % kRing);
+            const RowRing<IO, V, 2> ring{buf};
+            ring.wait();
+            xr[0] = ring.get(slot, 0);
+            if (mode_gate<MODE>(p)) gr[0] = ring.get(slot, 1);
+            slot = (slot + 1) % kRing;
+        }
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             gc[k] = gr[k];
@@ -274,7 +312,7 @@ __global__ void __launch_bounds__(kRowThreads, K == 1 ? kRowFwdBlocks : 1) norm_
                 if (t.has(k)) s = add(s, x[k][u]);
             }
         }
-        request(row + row_lanes, at + t.step);
+        if constexpr (!RING) request(row + row_lanes, at + t.step, 0);
         const float mean = lanes_sum<LG>(total(s)) * inv;
         U q = both<U>(0.f);
 #pragma unroll
@@ -314,26 +352,54 @@ __global__ void __launch_bounds__(kRowThreads, K == 1 ? kRowBwdBlocks : 1) norm_
     for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int u = 0; u < NU; ++u) sz[k][u] = szx[k][u] = both<U>(0.f);
+    constexpr bool RING = K == 1 && V > 1;
+    constexpr int AHEAD = RING ? kRing - 1 : 1;
+    __shared__ Pack<IO, V> buf[RING ? kRing : 1][3][RING ? kRowThreads : 1];
     Pack<IO, V> xr[K], dr[K], gr[K];
-    float mean_n = 0.f, rstd_n = 0.f;
-    auto request = [&](int row, long long at) {
-        if (!t.mine || row >= p.N) return;
-        mean_n = p.mean[(long long)row * p.G + t.g];
-        rstd_n = p.rstd[(long long)row * p.G + t.g];
+    float mean_n[AHEAD] = {}, rstd_n[AHEAD] = {};  // of the rows to come, the next one first
+    int slot = 0;
+    auto request = [&](int row, long long at, int to, float &mean, float &rstd) {
+        if (t.mine && row < p.N) {
+            mean = p.mean[(long long)row * p.G + t.g];
+            rstd = p.rstd[(long long)row * p.G + t.g];
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (t.has(k)) {
-                xr[k] = load_pack<IO, V>(p.x, at + k * LG * V);
-                dr[k] = load_pack<IO, V>(p.dy, at + k * LG * V);
-                if (mode_gate<MODE>(p)) gr[k] = load_pack<IO, V>(p.gate, at + k * LG * V);
-            }
+            for (int k = 0; k < K; ++k)
+                if (t.has(k)) {
+                    if constexpr (RING) {
+                        const RowRing<IO, V, 3> ring{buf};
+                        ring.copy(to, 0, p.x, at);
+                        ring.copy(to, 1, p.dy, at);
+                        if (mode_gate<MODE>(p)) ring.copy(to, 2, p.gate, at);
+                    } else {
+                        xr[k] = load_pack<IO, V>(p.x, at + k * LG * V);
+                        dr[k] = load_pack<IO, V>(p.dy, at + k * LG * V);
+                        if (mode_gate<MODE>(p)) gr[k] = load_pack<IO, V>(p.gate, at + k * LG * V);
+                    }
+                }
+        }
+        if constexpr (RING) RowRing<IO, V, 3>::commit();
     };
     long long at = t.base;
-    request(t.first, at);
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) request(t.first + k * row_lanes, at + k * t.step, k, mean_n[k], rstd_n[k]);
     for (int r0 = 0; r0 < p.N; r0 += row_lanes, at += t.step) {
         const int row = r0 + t.first;
         const bool live = t.mine && row < p.N;
-        const float mean = mean_n, rstd = rstd_n;
+        const float mean = mean_n[0], rstd = rstd_n[0];
+#pragma unroll
+        for (int k = 0; k + 1 < AHEAD; ++k) {
+            mean_n[k] = mean_n[k + 1];
+            rstd_n[k] = rstd_n[k + 1];
+        }
+        if constexpr (RING) {
+            request(row + AHEAD * row_lanes, at + AHEAD * t.step, (slot + AHEAD) % kRing, mean_n[AHEAD - 1], rstd_n[AHEAD - 1]);
+            const RowRing<IO, V, 3> ring{buf};
+            ring.wait();
+            xr[0] = ring.get(slot, 0);
+            dr[0] = ring.get(slot, 1);
+            if (mode_gate<MODE>(p)) gr[0] = ring.get(slot, 2);
+            slot = (slot + 1) % kRing;
+        }
         U xh[K][NU], dn[K][NU], s1 = both<U>(0.f), s2 = both<U>(0.f);
         Pack<IO, V> dg[K];
 #pragma unroll
@@ -353,7 +419,7 @@ __global__ void __launch_bounds__(kRowThreads, K == 1 ? kRowBwdBlocks : 1) norm_
             }
             if (mode_gate<MODE>(p)) store_pack<IO, V>(p.dgate, at + k * LG * V, dg[k]);
         }
-        request(row + row_lanes, at + t.step);
+        if constexpr (!RING) request(row + row_lanes, at + t.step, 0, mean_n[0], rstd_n[0]);
         const float m1 = lanes_sum<LG>(total(s1)) * inv, m2 = lanes_sum<LG>(total(s2)) * inv;
         if (!live) continue;
 #pragma unroll
@@ -415,7 +481,8 @@ __global__ void __launch_bounds__(1024) norm_channel_sum_kernel(const float *par
 
 constexpr int kTileThreads = 256;
 constexpr int kTileCols = 256;  // vector columns of a block
-constexpr int kTileAhead = 4, kGradAhead = 2;  // positions that a thread requests at a time
+// positions that a thread requests at a time: for the statistics, for the outputs, for the gradients
+constexpr int kStatAhead = 8, kTileAhead = 4, kGradAhead = 2;
 
 struct Stat {
     float n, mean, m2;
@@ -466,13 +533,13 @@ __global__ void __launch_bounds__(kTileThreads, 2) norm_tile_stats_kernel(NormAr
     float mean[V] = {}, m2[V] = {};
     float cnt = 0.f;
     if (t.live)
-        for (int s = t.s0 + t.rl; s < t.s1; s += kTileAhead * t.RL) {
-            Pack<IO, V> x[kTileAhead];
+        for (int s = t.s0 + t.rl; s < t.s1; s += kStatAhead * t.RL) {
+            Pack<IO, V> x[kStatAhead];
 #pragma unroll
-            for (int u = 0; u < kTileAhead; ++u)
+            for (int u = 0; u < kStatAhead; ++u)
                 if (s + u * t.RL < t.s1) x[u] = load_pack<IO, V>(p.x, t.at(p, s + u * t.RL));
 #pragma unroll
-            for (int u = 0; u < kTileAhead; ++u) {
+            for (int u = 0; u < kStatAhead; ++u) {
                 if (s + u * t.RL >= t.s1) break;
                 cnt += 1.f;
                 const float f = __fdividef(1.f, cnt);
@@ -512,21 +579,38 @@ __global__ void __launch_bounds__(kTileThreads, 2) norm_tile_stats_kernel(NormAr
     }
 }
 
-// mean and rstd of group g of sample n from all tiles' pieces, by one warp
-template <int V>
-__device__ __forceinline__ Stat merge_pieces(const NormArgs &p, int n, int g, int blocks) {
+// Visits the pieces of groups g0 .. g0 + 3 (as far as last) over all tiles, by one warp: f(k, a float pair,
+// the number of values behind it) for group g0 + k.  The groups' loads are independent of each other: four
+// at a time, one group after another took 6 us of a 20 us kernel.
+constexpr int kGroupsAtOnce = 4;
+
+template <int V, typename F>
+__device__ __forceinline__ void visit_pieces(const NormArgs &p, int n, int g0, int last, int blocks, F f) {
     const int D = p.C / p.G, lane = threadIdx.x & 31;
-    const int b0 = g * D / (kTileCols * V), b1 = ((g + 1) * D - 1) / (kTileCols * V), nb = b1 - b0 + 1;
-    Stat st{0.f, 0.f, 0.f};
-    for (int e = lane; e < p.tiles * nb; e += 32) {
-        const int tile = e / nb, cb = b0 + e % nb;
-        const int a = max(g * D, cb * kTileCols * V), b = min((g + 1) * D, (cb + 1) * kTileCols * V);
-        const int rows = (int)((long long)p.S * (tile + 1) / p.tiles) - (int)((long long)p.S * tile / p.tiles);
-        const float *in = p.stat_parts + 2 * (((long long)n * p.tiles + tile) * norm_pieces(p.G, blocks) + g + cb);
-        st = merge(st, Stat{(float)(b - a) * (float)rows, in[0], in[1]});
+    int first[kGroupsAtOnce], nb[kGroupsAtOnce], most = 0;
+#pragma unroll
+    for (int k = 0; k < kGroupsAtOnce; ++k) {
+        const int g = g0 + k;
+        first[k] = g * D / (kTileCols * V);
+        nb[k] = g <= last ? ((g + 1) * D - 1) / (kTileCols * V) - first[k] + 1 : 0;
+        most = max(most, nb[k]);
     }
-    for (int o = 16; o > 0; o >>= 1) st = merge(st, shfl(st, o));
-    return st;
+    for (int e = lane; e < p.tiles * most; e += 32) {
+        const int tile = e / most, j = e % most;
+        const int rows = (int)((long long)p.S * (tile + 1) / p.tiles) - (int)((long long)p.S * tile / p.tiles);
+        float2 x[kGroupsAtOnce];
+#pragma unroll
+        for (int k = 0; k < kGroupsAtOnce; ++k)
+            if (j < nb[k])
+                x[k] = reinterpret_cast<const float2 *>(p.stat_parts)[((long long)n * p.tiles + tile) * norm_pieces(p.G, blocks) + g0 + k + first[k] + j];
+#pragma unroll
+        for (int k = 0; k < kGroupsAtOnce; ++k)
+            if (j < nb[k]) {
+                const int cb = first[k] + j, g = g0 + k;
+                const int width = min((g + 1) * D, (cb + 1) * kTileCols * V) - max(g * D, cb * kTileCols * V);
+                f(k, x[k], (float)width * (float)rows);
+            }
+    }
 }
 
 template <typename IO, int V, int MODE>
@@ -534,15 +618,21 @@ __global__ void __launch_bounds__(kTileThreads, 2) norm_tile_apply_kernel(NormAr
     __shared__ float sh_mean[kTileCols * V], sh_rstd[kTileCols * V];
     const Tile<V> t(p, blockIdx.x);
     const int D = p.C / p.G, g0 = t.first_group(D);
-    for (int g = g0 + (threadIdx.x >> 5); g <= t.last_group(D); g += kTileThreads / 32) {
-        const Stat st = merge_pieces<V>(p, t.n, g, gridDim.y);
-        if ((threadIdx.x & 31) == 0) {
-            const float rstd = rsqrtf(st.m2 / ((float)D * (float)p.S) + p.eps);
-            sh_mean[g - g0] = st.mean;
-            sh_rstd[g - g0] = rstd;
-            if (t.tile == 0 && g * D >= t.c0) {  // the block with the group's first channel
-                if (p.mean) p.mean[(long long)t.n * p.G + g] = st.mean;
-                if (p.rstd) p.rstd[(long long)t.n * p.G + g] = rstd;
+    for (int g = g0 + kGroupsAtOnce * (threadIdx.x >> 5); g <= t.last_group(D); g += kGroupsAtOnce * (kTileThreads / 32)) {
+        Stat st[kGroupsAtOnce] = {};
+        visit_pieces<V>(p, t.n, g, t.last_group(D), gridDim.y,
+                        [&](int k, const float2 &x, float count) { st[k] = merge(st[k], Stat{count, x.x, x.y}); });
+#pragma unroll
+        for (int k = 0; k < kGroupsAtOnce; ++k) {
+            for (int o = 16; o > 0; o >>= 1) st[k] = merge(st[k], shfl(st[k], o));
+            if ((threadIdx.x & 31) == 0 && g + k <= t.last_group(D)) {
+                const float rstd = rsqrtf(st[k].m2 / ((float)D * (float)p.S) + p.eps);
+                sh_mean[g + k - g0] = st[k].mean;
+                sh_rstd[g + k - g0] = rstd;
+                if (t.tile == 0 && (g + k) * D >= t.c0) {  // the block with the group's first channel
+                    if (p.mean) p.mean[(long long)t.n * p.G + g + k] = st[k].mean;
+                    if (p.rstd) p.rstd[(long long)t.n * p.G + g + k] = rstd;
+                }
             }
         }
     }
@@ -674,19 +764,19 @@ __global__ void __launch_bounds__(kTileThreads, 2) norm_tile_grad_apply_kernel(N
     const Tile<V> t(p, blockIdx.x);
     const int D = p.C / p.G, g0 = t.first_group(D), lane = threadIdx.x & 31;
     const float inv = 1.f / ((float)D * (float)p.S);
-    for (int g = g0 + (threadIdx.x >> 5); g <= t.last_group(D); g += kTileThreads / 32) {
-        const int b0 = g * D / (kTileCols * V), b1 = ((g + 1) * D - 1) / (kTileCols * V), nb = b1 - b0 + 1;
-        float s1 = 0.f, s2 = 0.f;
-        for (int e = lane; e < p.tiles * nb; e += 32) {
-            const float *in = p.stat_parts + 2 * (((long long)t.n * p.tiles + e / nb) * norm_pieces(p.G, gridDim.y) + g + b0 + e % nb);
-            s1 += in[0];
-            s2 += in[1];
-        }
-        s1 = warp_sum(s1);
-        s2 = warp_sum(s2);
-        if (lane == 0) {
-            sh1[g - g0] = s1 * inv;
-            sh2[g - g0] = s2 * inv;
+    for (int g = g0 + kGroupsAtOnce * (threadIdx.x >> 5); g <= t.last_group(D); g += kGroupsAtOnce * (kTileThreads / 32)) {
+        float2 sum[kGroupsAtOnce] = {};
+        visit_pieces<V>(p, t.n, g, t.last_group(D), gridDim.y, [&](int k, const float2 &x, float) {
+            sum[k].x += x.x;
+            sum[k].y += x.y;
+        });
+#pragma unroll
+        for (int k = 0; k < kGroupsAtOnce; ++k) {
+            const float a = warp_sum(sum[k].x), b = warp_sum(sum[k].y);
+            if (lane == 0 && g + k <= t.last_group(D)) {
+                sh1[g + k - g0] = a * inv;
+                sh2[g + k - g0] = b * inv;
+            }
         }
     }
     __syncthreads();
