@@ -8,6 +8,7 @@ library is missing or the tensors are not on a CUDA device, the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -146,22 +147,24 @@ def status_string(status: int) -> str:
 
 
 def _ptr(x):
-    return None if x is None else ctypes.c_void_p(x.data_ptr())
+    return None if x is None else x.data_ptr()
 
 
 def _stream(stream, device):
     """The stream to launch on: the caller's (which must belong to `device`), else the current
     stream of `device` (not of whichever device happens to be current)."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
+        return torch._C._cuda_getCurrentRawStream(device.index)  # current_stream(device) without its object
+    if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def _call(device, fn, *args):
     """Run a library entry point with `device` current (the library launches on the current
     device and looks up per-device state there)."""
+    if torch.cuda.current_device() == device.index:
+        return fn(*args)
     with torch.cuda.device(device):
         return fn(*args)
 
@@ -175,7 +178,7 @@ def _check_tensor(name, x, dtype, shape, device):
         raise ValueError(f"{name} is on {x.device}, q is on {device}")
     if x.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
-    if tuple(x.shape) != tuple(shape):
+    if x.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(x.shape)}")
     if not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -482,17 +485,25 @@ def prism_state_fold(S_in, E, f, S_out=None, stream=None):
     return S_out
 
 
-def _scratch(size_fn, where, shape, device, workspace) -> torch.Tensor:
+@functools.lru_cache(maxsize=4096)
+def _scratch_bytes(entry, shape_type, fields, device_index) -> int:
+    """Workspace bytes of `entry` for a shape's values (the library's answer depends on them and on the
+    device's SM count alone)."""
+    need = ctypes.c_size_t(0)
+    shape = shape_type(*fields)
+    rc = _call(torch.device("cuda", device_index), getattr(load_library(), entry), ctypes.byref(shape), ctypes.byref(need))
+    if rc != PRISM_OK:
+        raise PrismError(rc, entry)
+    return need.value
+
+
+def _scratch(entry, shape, fields, device, workspace) -> torch.Tensor:
     """The caller's workspace, or a new one from torch's allocator: it belongs to this call alone, so
     calls on several streams, and captured graphs, never share one."""
     if workspace is not None:
         _check_tensor("workspace", workspace, torch.uint8, (workspace.numel(),), device)
         return workspace
-    need = ctypes.c_size_t(0)
-    rc = _call(device, size_fn, ctypes.byref(shape), ctypes.byref(need))
-    if rc != PRISM_OK:
-        raise PrismError(rc, where)
-    return torch.empty(need.value, dtype=torch.uint8, device=device)
+    return torch.empty(_scratch_bytes(entry, type(shape), fields, device.index), dtype=torch.uint8, device=device)
 
 
 def _launched_on(stream, device, *tensors) -> None:
@@ -504,26 +515,34 @@ def _launched_on(stream, device, *tensors) -> None:
                 t.record_stream(stream)
 
 
-def _check_view(name, x, dtype, shape, device):
-    """A tensor whose last dimension is dense and whose other strides are the library's to follow."""
+def _view_strides(name, x, dtype, shape, device):
+    """Checks a tensor whose last dimension is dense and whose other strides are the library's to follow;
+    returns those strides."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor (libprism has no CPU path)")
     if x.device != device:
         raise ValueError(f"{name} is on {x.device}, q is on {device}")
     if x.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
-    if tuple(x.shape) != tuple(shape):
+    if x.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(x.shape)}")
-    if x.stride(-1) != 1:
+    if x.is_contiguous():
+        return _DENSE
+    strides = x.stride()
+    if strides[-1] != 1:
         raise ValueError(f"{name} must have unit stride along its last dimension")
     unit = 16 // x.element_size()
-    for n, st in zip(x.shape[:-1], x.stride()[:-1]):
+    for n, st in zip(shape, strides[:-1]):
         if n > 1 and (st <= 0 or st % unit):
-            raise ValueError(f"{name}: strides must be positive multiples of 16 bytes, got {x.stride()} elements")
+            raise ValueError(f"{name}: strides must be positive multiples of 16 bytes, got {strides} elements")
+    return strides[:3]
+
+
+_DENSE = (0, 0, 0)  # prism_decay_shape: the dense layout
 
 
 def _decay_inputs(q, k, v, decay):
-    """Checks shared by the decay scan's entry points; returns (shape, device, io dtype)."""
+    """Checks shared by the decay scan's entry points; returns (shape, its sizes, device, io dtype)."""
     for name, x in (("q", q), ("k", k), ("v", v)):
         if not isinstance(x, torch.Tensor) or not x.is_cuda:
             raise TypeError(f"{name} must be a CUDA tensor (libprism has no CPU path)")
@@ -536,15 +555,13 @@ def _decay_inputs(q, k, v, decay):
     Hkv, dv = k.shape[2], v.shape[3]
     if Hkv < 1 or H % Hkv:
         raise ValueError(f"k has {Hkv} heads, which do not divide the {H} heads of q")
-    _check_view("q", q, io, (B, T, H, dk), dev)
-    _check_view("k", k, io, (B, T, Hkv, dk), dev)
-    _check_view("v", v, io, (B, T, Hkv, dv), dev)
-    _check_tensor("decay", decay, torch.float32, (H,), dev)
+    strides = (_view_strides("q", q, io, (B, T, H, dk), dev), _view_strides("k", k, io, (B, T, Hkv, dk), dev),
+               _view_strides("v", v, io, (B, T, Hkv, dv), dev))
     if decay is None:
         raise TypeError("decay must be a CUDA tensor (libprism has no CPU path)")
-    strides = [(ctypes.c_longlong * 3)(*x.stride()[:3]) for x in (q, k, v)]
-    shape = PrismDecayShape(B, H, T, Hkv, dk, dv, PRISM_F32 if io == torch.float32 else PRISM_BF16, *strides)
-    return shape, dev, io
+    _check_tensor("decay", decay, torch.float32, (H,), dev)
+    sizes = (B, H, T, Hkv, dk, dv, PRISM_F32 if io == torch.float32 else PRISM_BF16)
+    return PrismDecayShape(*sizes, *strides), sizes, dev, io
 
 
 def prism_decay_scan_fwd(q, k, v, decay, S0=None, lengths=None, *, o=None, S_final=None, want_state=True,
@@ -555,8 +572,8 @@ def prism_decay_scan_fwd(q, k, v, decay, S0=None, lengths=None, *, o=None, S_fin
     None; lengths: [B] int32 (valid tokens of a padded batch) or None.  Returns (o [B,T,H,dv], S_final
     [B,H,dv,dk] fp32 or None)."""
     lib = load_library()
-    shape, dev, io = _decay_inputs(q, k, v, decay)
-    B, T, H, dk, dv = shape.B, shape.T, shape.H, shape.dk, shape.dv
+    shape, sizes, dev, io = _decay_inputs(q, k, v, decay)
+    B, H, T, Hkv, dk, dv, _ = sizes
     f32 = torch.float32
     _check_tensor("S0", S0, f32, (B, H, dv, dk), dev)
     _check_tensor("lengths", lengths, torch.int32, (B,), dev)
@@ -566,7 +583,7 @@ def prism_decay_scan_fwd(q, k, v, decay, S0=None, lengths=None, *, o=None, S_fin
     if S_final is None and want_state:
         S_final = torch.empty((B, H, dv, dk), dtype=f32, device=dev)
     _check_tensor("S_final", S_final, f32, (B, H, dv, dk), dev)
-    ws = _scratch(lib.prism_decay_scan_fwd_workspace_size, "prism_decay_scan_fwd_workspace_size", shape, dev, workspace)
+    ws = _scratch("prism_decay_scan_fwd_workspace_size", shape, sizes, dev, workspace)
     rc = _call(dev, lib.prism_decay_scan_fwd, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(S0),
                _ptr(lengths), _ptr(o), _ptr(S_final), _ptr(ws), ctypes.c_size_t(ws.numel()), _stream(stream, dev))
     if rc != PRISM_OK:
@@ -581,8 +598,8 @@ def prism_decay_scan_bwd(q, k, v, decay, S0=None, lengths=None, *, dO, dS_final=
     [B,H,dv,dk] fp32 or None.  Returns a dict with dq [B,T,H,dk], dk [B,T,Hkv,dk], dv [B,T,Hkv,dv] in
     the inputs' type and dS0 [B,H,dv,dk] fp32 (or None)."""
     lib = load_library()
-    shape, dev, io = _decay_inputs(q, k, v, decay)
-    B, T, H, dk, dv = shape.B, shape.T, shape.H, shape.dk, shape.dv
+    shape, sizes, dev, io = _decay_inputs(q, k, v, decay)
+    B, H, T, Hkv, dk, dv, _ = sizes
     f32 = torch.float32
     _check_tensor("S0", S0, f32, (B, H, dv, dk), dev)
     _check_tensor("lengths", lengths, torch.int32, (B,), dev)
@@ -591,10 +608,10 @@ def prism_decay_scan_bwd(q, k, v, decay, S0=None, lengths=None, *, dO, dS_final=
     _check_tensor("dO", dO, io, (B, T, H, dv), dev)
     _check_tensor("dS_final", dS_final, f32, (B, H, dv, dk), dev)
     out = {"dq": torch.empty((B, T, H, dk), dtype=io, device=dev),
-           "dk": torch.empty((B, T, shape.Hkv, dk), dtype=io, device=dev),
-           "dv": torch.empty((B, T, shape.Hkv, dv), dtype=io, device=dev),
+           "dk": torch.empty((B, T, Hkv, dk), dtype=io, device=dev),
+           "dv": torch.empty((B, T, Hkv, dv), dtype=io, device=dev),
            "dS0": torch.empty((B, H, dv, dk), dtype=f32, device=dev) if want_dS0 else None}
-    ws = _scratch(lib.prism_decay_scan_bwd_workspace_size, "prism_decay_scan_bwd_workspace_size", shape, dev, workspace)
+    ws = _scratch("prism_decay_scan_bwd_workspace_size", shape, sizes, dev, workspace)
     rc = _call(dev, lib.prism_decay_scan_bwd, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(S0),
                _ptr(lengths), _ptr(dO), _ptr(dS_final), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
                _ptr(out["dS0"]), _ptr(ws), ctypes.c_size_t(ws.numel()), _stream(stream, dev))
@@ -608,8 +625,8 @@ def prism_decay_step(q, k, v, decay, S, *, o=None, stream=None):
     """One token of the decay scan, S [B,H,dv,dk] fp32 updated in place.  q: [B,1,H,dk]; k, v: [B,1,Hkv,dk],
     [B,1,Hkv,dv] (views as for prism_decay_scan_fwd); decay: [H] fp32.  Returns o [B,1,H,dv]."""
     lib = load_library()
-    shape, dev, io = _decay_inputs(q, k, v, decay)
-    B, T, H, dk, dv = shape.B, shape.T, shape.H, shape.dk, shape.dv
+    shape, sizes, dev, io = _decay_inputs(q, k, v, decay)
+    B, H, T, Hkv, dk, dv, _ = sizes
     if S is None:
         raise TypeError("S must be a CUDA tensor (libprism has no CPU path)")
     _check_tensor("S", S, torch.float32, (B, H, dv, dk), dev)
@@ -625,7 +642,7 @@ def prism_decay_step(q, k, v, decay, S, *, o=None, stream=None):
 
 
 def _norm_inputs(x, groups, weight, bias, gate, eps, activation):
-    """Checks shared by the group norm's entry points; returns (shape, device, io dtype)."""
+    """Checks shared by the group norm's entry points; returns (shape, its values, device, io dtype)."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise TypeError("x must be a CUDA tensor (libprism has no CPU path)")
     if x.dim() < 2:
@@ -647,8 +664,8 @@ def _norm_inputs(x, groups, weight, bias, gate, eps, activation):
     _check_tensor("weight", weight, torch.float32, (C,), dev)
     _check_tensor("bias", bias, torch.float32, (C,), dev)
     _check_tensor("gate", gate, io, x.shape, dev)
-    shape = PrismNormShape(N, S, C, groups, PRISM_F32 if io == torch.float32 else PRISM_BF16, ACTIVATIONS[activation], eps)
-    return shape, dev, io
+    sizes = (N, S, C, groups, PRISM_F32 if io == torch.float32 else PRISM_BF16, ACTIVATIONS[activation], float(eps))
+    return PrismNormShape(*sizes), sizes, dev, io
 
 
 def prism_group_norm_fwd(x, groups, weight=None, bias=None, gate=None, *, eps=1e-5, activation="none", y=None,
@@ -659,13 +676,13 @@ def prism_group_norm_fwd(x, groups, weight=None, bias=None, gate=None, *, eps=1e
     the result, or of the gate that multiplies it.  Returns (y, mean, rstd), the last two [N, groups]
     fp32 for prism_group_norm_bwd."""
     lib = load_library()
-    shape, dev, io = _norm_inputs(x, groups, weight, bias, gate, eps, activation)
+    shape, sizes, dev, io = _norm_inputs(x, groups, weight, bias, gate, eps, activation)
     if y is None:
         y = torch.empty_like(x)
     _check_tensor("y", y, io, x.shape, dev)
-    mean = torch.empty((shape.N, groups), dtype=torch.float32, device=dev)
+    mean = torch.empty((sizes[0], groups), dtype=torch.float32, device=dev)
     rstd = torch.empty_like(mean)
-    ws = _scratch(lib.prism_group_norm_fwd_workspace_size, "prism_group_norm_fwd_workspace_size", shape, dev, workspace)
+    ws = _scratch("prism_group_norm_fwd_workspace_size", shape, sizes, dev, workspace)
     rc = _call(dev, lib.prism_group_norm_fwd, ctypes.byref(shape), _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate),
                _ptr(y), _ptr(mean), _ptr(rstd), _ptr(ws), ctypes.c_size_t(ws.numel()), _stream(stream, dev))
     if rc != PRISM_OK:
@@ -679,13 +696,13 @@ def prism_group_norm_bwd(x, groups, mean, rstd, weight=None, bias=None, gate=Non
     """Backward of prism_group_norm_fwd: its inputs, the mean and rstd it returned, and dy like x.  Returns
     a dict with dx, and dgate, dweight, dbias where gate, weight, bias are given."""
     lib = load_library()
-    shape, dev, io = _norm_inputs(x, groups, weight, bias, gate, 0.0, activation)
+    shape, sizes, dev, io = _norm_inputs(x, groups, weight, bias, gate, 0.0, activation)
     for name, t in (("mean", mean), ("rstd", rstd), ("dy", dy)):
         if t is None:
             raise TypeError(f"{name} must be a CUDA tensor (libprism has no CPU path)")
     f32 = torch.float32
-    _check_tensor("mean", mean, f32, (shape.N, groups), dev)
-    _check_tensor("rstd", rstd, f32, (shape.N, groups), dev)
+    _check_tensor("mean", mean, f32, (sizes[0], groups), dev)
+    _check_tensor("rstd", rstd, f32, (sizes[0], groups), dev)
     _check_tensor("dy", dy, io, x.shape, dev)
     out = {"dx": torch.empty_like(x)}
     if gate is not None:
@@ -694,7 +711,7 @@ def prism_group_norm_bwd(x, groups, mean, rstd, weight=None, bias=None, gate=Non
         out["dweight"] = torch.empty_like(weight)
     if bias is not None:
         out["dbias"] = torch.empty_like(bias)
-    ws = _scratch(lib.prism_group_norm_bwd_workspace_size, "prism_group_norm_bwd_workspace_size", shape, dev, workspace)
+    ws = _scratch("prism_group_norm_bwd_workspace_size", shape, sizes, dev, workspace)
     rc = _call(dev, lib.prism_group_norm_bwd, ctypes.byref(shape), _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate),
                _ptr(mean), _ptr(rstd), _ptr(dy), _ptr(out["dx"]), _ptr(out.get("dgate")), _ptr(out.get("dweight")),
                _ptr(out.get("dbias")), _ptr(ws), ctypes.c_size_t(ws.numel()), _stream(stream, dev))
