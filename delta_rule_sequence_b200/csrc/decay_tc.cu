@@ -10,7 +10,7 @@
 // state sums thousands of them.  It is split into bf16 terms whose sum has 16 (pass kernel: only outputs
 // depend on it) or 24 bits (sum kernel: the fp32 states that the caller gets), each multiplied with the exact Z.
 // The state is rounded to bf16 once per chunk as the B operand of X R^T; its fp32 master stays in
-// registers, so that no tensor-core accumulation runs longer than one chunk.
+// registers, so that no tensor-core accumulation (which truncates) runs longer than one chunk.
 //
 // Widths of 32 run as 64: the TMA boxes reach past the tensor, where loads give zeros and stores
 // write nothing.
@@ -25,6 +25,9 @@ namespace {
 using namespace tc;
 
 constexpr int CT = kDecayChunkTc;
+
+// Polls of a bounded wait (of up to kSuspendNs each), and in the stall test.
+constexpr uint32_t kPolls = 1u << 17, kStallPolls = 1u << 6;
 
 // Library status word of these kernels (a bounded wait that gave up), read and cleared by
 // prism_query_device_status.
@@ -84,39 +87,41 @@ struct Powers {
     __device__ __forceinline__ float at(int e) const { return p[e]; }
 };
 
-// Column m of the Y tile, tokens j0 .. j0 + 31, times their weights w, as TERMS bf16 terms into this
+// Column m of the Y tile, tokens j0 .. j0 + 15, times their weights w, as TERMS bf16 terms into this
 // thread's TMEM lane: term t at column col + 64 t, two tokens per column.  Tokens from n on are zero
 // whatever the tile holds there.
+constexpr int kWeigh = 16;
+
 template <int TERMS>
-__device__ __forceinline__ void weigh32(const uint8_t *Y, int m, const float *w, int j0, int n, uint32_t taddr_lane, int col) {
-    const uint8_t *base = Y + (m >> 6) * kBlk + ((m & 7) << 1);
+__device__ __forceinline__ void weigh(const uint8_t *Y, int m, const float *w, int j0, int n, uint32_t taddr_lane, int col) {
+    const uint8_t *base = Y + (m >> 6) * kBlk + ((m & 7) << 1) + j0 * 128;
     const int ch = (m & 63) >> 3;
-    float x[32];
+    float x[kWeigh];
 #pragma unroll
-    for (int i = 0; i < 32; i += 4) {
+    for (int i = 0; i < kWeigh; i += 4) {
         const float4 w4 = *reinterpret_cast<const float4 *>(w + j0 + i);
         const float *wf = &w4.x;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int j = i + e;  // (j0 is a multiple of 8: it does not change the swizzle)
-            const uint32_t raw = *reinterpret_cast<const uint16_t *>(base + (j0 + j) * 128 + ((ch ^ (j & 7)) << 4));
+            const uint32_t raw = *reinterpret_cast<const uint16_t *>(base + j * 128 + ((ch ^ (j & 7)) << 4));
             x[j] = __uint_as_float(raw << 16) * wf[e];
         }
     }
-    if (j0 + 32 > n) {
+    if (j0 + kWeigh > n) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = j0 + j < n ? x[j] : 0.f;
+        for (int j = 0; j < kWeigh; ++j) x[j] = j0 + j < n ? x[j] : 0.f;
     }
 #pragma unroll
     for (int k = 0; k < TERMS; ++k) {
-        uint32_t t[16];
+        uint32_t t[kWeigh / 2];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < kWeigh / 2; ++i) {
             t[i] = bf16_pair(x[2 * i], x[2 * i + 1]);
             x[2 * i] -= lo_f(t[i]);
             x[2 * i + 1] -= hi_f(t[i]);
         }
-        tmem_st16(taddr_lane + col + 64 * k + j0 / 2, t);
+        tmem_st8(taddr_lane + col + 64 * k + j0 / 2, t);
     }
 }
 
@@ -160,7 +165,7 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Walk wk(p);
     uint32_t *status = &g_decay_status;
-    const uint32_t lim = p.stall ? kStallTestPolls : kWaitPolls;
+    const uint32_t lim = p.stall ? kStallPolls : kPolls;
     const float a = p.decay[wk.h];
 
     if (warp == LY::MMAW) tmem_alloc(&tmem_base_sh, 512);
@@ -193,7 +198,7 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
             int i = 0;
             for (; i < wk.nch; ++i) {
                 const int st = i % NST;
-                if (i >= NST && !mbar_wait(&freeb[st], (uint32_t)((i / NST - 1) & 1), status, lim)) break;
+                if (i >= NST && !mbar_wait_suspend(&freeb[st], (uint32_t)((i / NST - 1) & 1), status, lim)) break;
                 uint8_t *s = sm + st * LY::STAGE;
                 mbar_expect_tx(&full[st], LY::STAGE);
                 for (int c = 0; c < D1 / 64; ++c) tma_load_4d(s + c * kBlk, &maps.y, 64 * c, wk.h / p.y.div, wk.t0(i), wk.b, &full[st]);
@@ -201,39 +206,40 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
                     tma_load_4d(s + tile_bytes<D1>() + c * kBlk, &maps.z, 64 * c, wk.h / p.z.div, wk.t0(i), wk.b, &full[st]);
             }
             // loads in flight land before the CTA exits
-            for (int k = i > NST ? i - NST : 0; k < i; ++k) mbar_wait(&full[k % NST], (uint32_t)((k / NST) & 1), nullptr, lim);
+            for (int k = i > NST ? i - NST : 0; k < i; ++k) mbar_wait_suspend(&full[k % NST], (uint32_t)((k / NST) & 1), nullptr, lim);
         }
     } else if (warp == LY::MMAW) {
-        if (lane == 0) {
+        {
             const uint32_t id = idesc_bf16(128, D2, 0, 1);
             auto oz = [](int ks) { return (uint64_t)koff_mn_sw128(ks); };
+            auto oy = [](int ks) { return 8 * ks; };
             for (int i = 0; i < wk.nch; ++i) {
                 const int st = i % NST, pb = i & 1;
-                if (!mbar_wait(&full[st], (uint32_t)((i / NST) & 1), status, lim) ||
-                    !mbar_wait(&yp_full[pb], (uint32_t)((i >> 1) & 1), status, lim) ||
-                    (i > 0 && !mbar_wait(&d_free, (uint32_t)((i - 1) & 1), status, lim)))
+                if (!mbar_wait_suspend(&full[st], (uint32_t)((i / NST) & 1), status, lim) ||
+                    !mbar_wait_suspend(&yp_full[pb], (uint32_t)((i >> 1) & 1), status, lim) ||
+                    (i > 0 && !mbar_wait_suspend(&d_free, (uint32_t)((i - 1) & 1), status, lim)))
                     break;
                 fence_after_sync();
                 const uint64_t dz = make_desc(smem_u32(sm + st * LY::STAGE + tile_bytes<D1>()), kBlk, 1024, 2);
                 const uint32_t ya = tb + LY::cY + pb * 192;
                 // smallest terms first: their sum loses nothing to the large one's magnitude
-                mma_steps_tmem_a<CT / 16>(tb + LY::cD, id, ya + 128, dz, oz, false);
-                mma_steps_tmem_a<CT / 16>(tb + LY::cD, id, ya + 64, dz, oz, true);
-                mma_steps_tmem_a<CT / 16>(tb + LY::cD, id, ya, dz, oz, true);
-                mma_commit(&d_full);
-                mma_commit(&yp_free[pb]);
-                mma_commit(&freeb[st]);
+                mma_steps_tmem_a_warp<CT / 16>(tb + LY::cD, id, ya + 128, dz, oy, oz, false);
+                mma_steps_tmem_a_warp<CT / 16>(tb + LY::cD, id, ya + 64, dz, oy, oz, true);
+                mma_steps_tmem_a_warp<CT / 16>(tb + LY::cD, id, ya, dz, oy, oz, true);
+                mma_commit_warp(&d_full);
+                mma_commit_warp(&yp_free[pb]);
+                mma_commit_warp(&freeb[st]);
             }
-            mma_commit(&drain);
-            mbar_wait(&drain, 0, nullptr, lim);
+            mma_commit_warp(&drain);
+            mbar_wait_suspend(&drain, 0, nullptr, lim);
         }
     } else if (warp < LY::YW) {
         const int q = warp & 3, half = warp >> 2, m = 32 * q + lane;
         for (int i = 0; i < wk.nch; ++i) {
             const int st = i % NST, pb = i & 1, n = wk.n(i);
             uint8_t *s = sm + st * LY::STAGE;
-            if (!mbar_wait(&full[st], (uint32_t)((i / NST) & 1), status, lim) ||
-                (i >= 2 && !mbar_wait(&yp_free[pb], (uint32_t)(((i >> 1) - 1) & 1), status, lim)))
+            if (!mbar_wait_suspend(&full[st], (uint32_t)((i / NST) & 1), status, lim) ||
+                (i >= 2 && !mbar_wait_suspend(&yp_free[pb], (uint32_t)(((i >> 1) - 1) & 1), status, lim)))
                 break;
             fence_after_sync();
             if (n < CT) {
@@ -243,8 +249,8 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
             if (32 * q < D1) {
                 const float *w = i + 1 < wk.nch ? pw.w : w_last;
 #pragma unroll 1
-                for (int j0 = 64 * half; j0 < 64 * half + 64; j0 += 32)
-                    weigh32<3>(s, m, w, j0, n, taddr(tb, 32 * q, 0), LY::cY + pb * 192);
+                for (int j0 = 64 * half; j0 < 64 * half + 64; j0 += kWeigh)
+                    weigh<3>(s, m, w, j0, n, taddr(tb, 32 * q, 0), LY::cY + pb * 192);
                 tmem_wait_st();
             }
             fence_before_sync();
@@ -263,7 +269,7 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
         bool ok = true;
         for (int i = 0; i < wk.nch; ++i) {
             const float an = pw.at(wk.n(i));
-            if (!mbar_wait(&d_full, (uint32_t)(i & 1), status, lim)) { ok = false; break; }
+            if (!mbar_wait_suspend(&d_full, (uint32_t)(i & 1), status, lim)) { ok = false; break; }
             fence_after_sync();
             if (32 * q < D1) {
 #pragma unroll
@@ -299,9 +305,15 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
 
 template <int D1, int D2>
 struct PassLayout {
-    static constexpr int PW = 4, OW = 4, SW = 8, YW = 4;  // warps: P', outputs, state, weighted Y
+    static constexpr int PW = 8, OW = 4, SW = 8, YW = 8;  // warps: P', outputs, state, weighted Y
     static constexpr int OW0 = PW, SW0 = OW0 + OW, YW0 = SW0 + SW, LOADW = YW0 + YW, MMAW = LOADW + 1;
-    static constexpr int THREADS = 32 * (MMAW + 1);
+    static constexpr int THREADS = 32 * (LOADW + 4);      // whole warpgroups: two warps of the last have no role
+    // Registers of a thread by role: the block is launched with 64 each, and what the others give up is what the
+    // state warps, which hold D2 / 2 state elements, take on.  A launch is refused where the shares add up to more
+    // than the kernel was built with (setmaxnreg would wait for registers that never come).
+    static constexpr int RS = 96, RP = 56, RO = 56, RY = 56, RM = 40;
+    static constexpr int SHARES = (SW * RS + PW * RP + OW * RO + YW * RY + 4 * RM) * 32;
+    static_assert(THREADS == 1024 && SHARES <= 64 * THREADS, "register shares");
     static constexpr int NST = D1 == 64 ? (D2 == 64 ? 4 : 3) : 2;
     static constexpr uint32_t X = 0, Y = tile_bytes<D1>(), Z = 2 * tile_bytes<D1>();
     static constexpr uint32_t STAGE = 2 * tile_bytes<D1>() + tile_bytes<D2>();
@@ -327,7 +339,7 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Walk wk(p);
     uint32_t *status = &g_decay_status;
-    const uint32_t lim = p.stall ? kStallTestPolls : kWaitPolls;
+    const uint32_t lim = p.stall ? kStallPolls : kPolls;
     const float a = p.decay[wk.h];
 
     if (warp == LY::MMAW) tmem_alloc(&tmem_base_sh, 512);
@@ -359,6 +371,7 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
     fence_after_sync();
     const uint32_t tb = tmem_base_sh;
 
+    if (warp >= LY::LOADW) setmaxnreg_dec<LY::RM>();
     if (warp == LY::LOADW) {
         if (lane == 0 && !p.stall) {
             int i = 0;
@@ -368,26 +381,28 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
                 const int st = i % NST;
                 const uint32_t par = (uint32_t)((i / NST - 1) & 1);
                 uint8_t *s = sm + st * LY::STAGE;
-                if (i >= NST && !mbar_wait(&x_free[st], par, status, lim)) { ok = false; break; }
+                if (i >= NST && !mbar_wait_suspend(&x_free[st], par, status, lim)) { ok = false; break; }
                 load_tile(s + LY::X, &maps.x, D1, wk.h / p.x.div, wk.t0(i), wk.b, &x_full[st]);
                 ++nx;
-                if (i >= NST && !mbar_wait(&y_free[st], par, status, lim)) { ok = false; break; }
+                if (i >= NST && !mbar_wait_suspend(&y_free[st], par, status, lim)) { ok = false; break; }
                 load_tile(s + LY::Y, &maps.y, D1, wk.h / p.y.div, wk.t0(i), wk.b, &y_full[st]);
                 ++ny;
-                if (i >= NST && !mbar_wait(&z_free[st], par, status, lim)) { ok = false; break; }
+                if (i >= NST && !mbar_wait_suspend(&z_free[st], par, status, lim)) { ok = false; break; }
                 load_tile(s + LY::Z, &maps.z, D2, wk.h / p.z.div, wk.t0(i), wk.b, &z_full[st]);
                 ++nz;
             }
             // loads in flight land before the CTA exits
-            for (int k = nx > NST ? nx - NST : 0; k < nx; ++k) mbar_wait(&x_full[k % NST], (uint32_t)((k / NST) & 1), nullptr, lim);
-            for (int k = ny > NST ? ny - NST : 0; k < ny; ++k) mbar_wait(&y_full[k % NST], (uint32_t)((k / NST) & 1), nullptr, lim);
-            for (int k = nz > NST ? nz - NST : 0; k < nz; ++k) mbar_wait(&z_full[k % NST], (uint32_t)((k / NST) & 1), nullptr, lim);
+            for (int k = nx > NST ? nx - NST : 0; k < nx; ++k) mbar_wait_suspend(&x_full[k % NST], (uint32_t)((k / NST) & 1), nullptr, lim);
+            for (int k = ny > NST ? ny - NST : 0; k < ny; ++k) mbar_wait_suspend(&y_full[k % NST], (uint32_t)((k / NST) & 1), nullptr, lim);
+            for (int k = nz > NST ? nz - NST : 0; k < nz; ++k) mbar_wait_suspend(&z_full[k % NST], (uint32_t)((k / NST) & 1), nullptr, lim);
         }
     } else if (warp == LY::MMAW) {
-        if (lane == 0) {
+        {
             const uint32_t idP = idesc_bf16(128, 128, 0, 0), idZ = idesc_bf16(128, D2, 0, 1);
             auto ok_ = [](int ks) { return (uint64_t)koff_k_sw128(ks, kBlk); };
             auto omn = [](int ks) { return (uint64_t)koff_mn_sw128(ks); };
+            auto oy = [](int ks) { return 8 * ks; };
+            auto op = [](int ks) { return 8 * ks + (ks >= 4 ? 32 : 0); };  // P': 64 tokens in each half of P
             const uint64_t dR = make_desc(smem_u32(sm + LY::R), LY::R_BLK, 1024, 2);
             for (int i = 0; i < wk.nch; ++i) {
                 const int st = i % NST;
@@ -395,69 +410,74 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
                 const uint32_t s = smem_u32(sm + st * LY::STAGE);
                 const uint64_t dX = make_desc(s + LY::X, 16, 1024, 2), dY = make_desc(s + LY::Y, 16, 1024, 2),
                                dZ = make_desc(s + LY::Z, kBlk, 1024, 2);
-                if (!mbar_wait(&x_full[st], par, status, lim) || !mbar_wait(&y_full[st], par, status, lim)) break;
+                if (!mbar_wait_suspend(&x_full[st], par, status, lim) || !mbar_wait_suspend(&y_full[st], par, status, lim)) break;
                 fence_after_sync();
                 // P (its region's last readers were the previous chunk's P' Z products, issued before)
-                mma_steps<D1 / 16>(tb + LY::cP, idP, dX, dY, ok_, ok_, false);
-                mma_commit(&p_full);
-                mma_commit(&y_free[st]);
+                mma_steps_warp<D1 / 16>(tb + LY::cP, idP, dX, dY, ok_, ok_, false);
+                mma_commit_warp(&p_full);
+                mma_commit_warp(&y_free[st]);
                 // X R^T
-                if (!mbar_wait(&s_ready, ph, status, lim) || (i > 0 && !mbar_wait(&o_free, before, status, lim))) break;
+                if (!mbar_wait_suspend(&s_ready, ph, status, lim) || (i > 0 && !mbar_wait_suspend(&o_free, before, status, lim))) break;
                 fence_after_sync();
-                mma_steps<D1 / 16>(tb + LY::cO, idZ, dX, dR, ok_, omn, false);
-                mma_commit(&qs_full);
-                mma_commit(&x_free[st]);
+                mma_steps_warp<D1 / 16>(tb + LY::cO, idZ, dX, dR, ok_, omn, false);
+                mma_commit_warp(&qs_full);
+                mma_commit_warp(&x_free[st]);
                 // the write (the state warps have read the last one: s_ready)
-                if (!mbar_wait(&yp_full, ph, status, lim) || !mbar_wait(&z_full[st], par, status, lim)) break;
+                if (!mbar_wait_suspend(&yp_full, ph, status, lim) || !mbar_wait_suspend(&z_full[st], par, status, lim)) break;
                 fence_after_sync();
                 if (i + 1 < wk.nch) {
-                    mma_steps_tmem_a<CT / 16>(tb + LY::cD, idZ, tb + LY::cY + 64, dZ, omn, false);
-                    mma_steps_tmem_a<CT / 16>(tb + LY::cD, idZ, tb + LY::cY, dZ, omn, true);
-                    mma_commit(&ds_full);
-                    mma_commit(&yp_free);
+                    mma_steps_tmem_a_warp<CT / 16>(tb + LY::cD, idZ, tb + LY::cY + 64, dZ, oy, omn, false);
+                    mma_steps_tmem_a_warp<CT / 16>(tb + LY::cD, idZ, tb + LY::cY, dZ, oy, omn, true);
+                    mma_commit_warp(&ds_full);
+                    mma_commit_warp(&yp_free);
                 }
                 // O += P' Z
-                if (!mbar_wait(&p_ready, ph, status, lim) || !mbar_wait(&o_scaled, ph, status, lim)) break;
+                if (!mbar_wait_suspend(&p_ready, ph, status, lim) || !mbar_wait_suspend(&o_scaled, ph, status, lim)) break;
                 fence_after_sync();
-                mma_steps_tmem_a<CT / 16>(tb + LY::cO, idZ, tb + LY::cP, dZ, omn, true);
-                mma_commit(&o_full);
+                mma_steps_tmem_a_warp<CT / 16>(tb + LY::cO, idZ, tb + LY::cP, dZ, op, omn, true);
+                mma_commit_warp(&o_full);
             }
-            mma_commit(&drain);
-            mbar_wait(&drain, 0, nullptr, lim);
+            mma_commit_warp(&drain);
+            mbar_wait_suspend(&drain, 0, nullptr, lim);
         }
+    } else if (warp > LY::MMAW) {
+        // (no role)
     } else if (warp < LY::OW0) {
-        // ---------------- P' = a^|i-j| P on the causal side, as bf16 over P's first 64 columns ----------------
-        const int q = warp, row = 32 * q + lane;
+        setmaxnreg_dec<LY::RP>();
+        // ---------------- P' = a^|i-j| P on the causal side, as bf16 over P ----------------
+        // two warps per 32 rows, 64 columns each, whose bf16 values go to the first 32 of the warp's own
+        const int q = warp & 3, half = warp >> 2, row = 32 * q + lane;
         const uint32_t tl = taddr(tb, 32 * q, LY::cP);
         for (int i = 0; i < wk.nch; ++i) {
             const int n = wk.n(i);
-            if (!mbar_wait(&p_full, (uint32_t)(i & 1), status, lim)) break;
+            if (!mbar_wait_suspend(&p_full, (uint32_t)(i & 1), status, lim)) break;
             fence_after_sync();
-            // 32 columns at a time, in a loop: unrolled, the five roles' code of a chunk no longer fits the
-            // instruction cache and every role waits for its instructions (P' took 7000 cycles instead of 900)
+            // 16 columns at a time, in a loop: unrolled, the five roles' code of a chunk no longer fits the
+            // instruction cache and every role waits for its instructions (P' took 7000 cycles instead of 1400)
 #pragma unroll 1
-            for (int J = 0; J < 4; ++J) {
-                uint32_t out[16];
+            for (int c0 = 64 * half; c0 < 64 * half + 64; c0 += 16) {
+                const int J = c0 >> 5, j0 = c0 & 31;  // 32-column block, and the columns' place in it
+                uint32_t out[8];
                 if (J == q || (wk.reverse ? J > q : J < q)) {
-                    float v[32];
-                    tmem_ld32(tl + 32 * J, v);
+                    float v[16];
+                    tmem_ld16(tl + c0, v);
                     tmem_wait_ld();
                     if (J == q) {
                         // (the powers of the other side of the diagonal are zeros below the table)
-                        const float *d = pw.p + (wk.reverse ? -lane : lane);
+                        const float *d = pw.p + (wk.reverse ? j0 - lane : lane - j0);
                         if (wk.reverse) {
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) v[c] *= d[c];
+                            for (int c = 0; c < 16; ++c) v[c] *= d[c];
                         } else {
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) v[c] *= d[-c];
+                            for (int c = 0; c < 16; ++c) v[c] *= d[-c];
                         }
                     } else {
                         // a^|row - col| = a^(distance to the block's near column) x a^(near column - col)
                         const float f = pw.at(wk.reverse ? 32 * J - row : row - 32 * J - 31);
-                        const float *near = wk.reverse ? pw.p : pw.w + CT - 32;  // a^c, a^(31 - c)
+                        const float *near = (wk.reverse ? pw.p : pw.w + CT - 32) + j0;  // a^c, a^(31 - c)
 #pragma unroll
-                        for (int c = 0; c < 32; c += 4) {
+                        for (int c = 0; c < 16; c += 4) {
                             const float4 u = *reinterpret_cast<const float4 *>(near + c);
                             v[c] *= f * u.x;
                             v[c + 1] *= f * u.y;
@@ -465,17 +485,17 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
                             v[c + 3] *= f * u.w;
                         }
                     }
-                    if (32 * J + 32 > n) {
+                    if (c0 + 16 > n) {
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) v[c] = 32 * J + c < n ? v[c] : 0.f;
+                        for (int c = 0; c < 16; ++c) v[c] = c0 + c < n ? v[c] : 0.f;
                     }
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) out[c] = bf16_pair(v[2 * c], v[2 * c + 1]);
+                    for (int c = 0; c < 8; ++c) out[c] = bf16_pair(v[2 * c], v[2 * c + 1]);
                 } else {
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) out[c] = 0u;
+                    for (int c = 0; c < 8; ++c) out[c] = 0u;
                 }
-                tmem_st16(tl + 16 * J, out);  // columns that this lane has read already
+                tmem_st8(tl + 64 * half + ((c0 & 63) >> 1), out);  // columns that this lane has read already
             }
             tmem_wait_st();
             fence_before_sync();
@@ -483,6 +503,7 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
             if (lane == 0) mbar_arrive(&p_ready);
         }
     } else if (warp < LY::SW0) {
+        setmaxnreg_dec<LY::RO>();
         // ---------------- outputs ----------------
         const int q = warp & 3, row = 32 * q + lane;
         const uint32_t tl = taddr(tb, 32 * q, LY::cO);
@@ -490,43 +511,43 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
             const int n = wk.n(i), t0 = wk.t0(i), st = i % NST;
             const bool live = row < n;
             const float f = live ? pw.at(wk.reverse ? n - 1 - row : row + 1) : 0.f;
-            if (!mbar_wait(&qs_full, (uint32_t)(i & 1), status, lim)) break;
+            if (!mbar_wait_suspend(&qs_full, (uint32_t)(i & 1), status, lim)) break;
             fence_after_sync();
 #pragma unroll 1
-            for (int c = 0; c < D2; c += 32) {
-                float v[32];
-                tmem_ld32(tl + c, v);
+            for (int c = 0; c < D2; c += 16) {
+                float v[16];
+                tmem_ld16(tl + c, v);
                 tmem_wait_ld();
-                uint32_t u[32];
+                uint32_t u[16];
 #pragma unroll
-                for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(v[k] * f);
-                tmem_st32(tl + c, u);
+                for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(v[k] * f);
+                tmem_st16(tl + c, u);
             }
             tmem_wait_st();
             fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&o_scaled);
-            if (!mbar_wait(&o_full, (uint32_t)(i & 1), status, lim)) break;
+            if (!mbar_wait_suspend(&o_full, (uint32_t)(i & 1), status, lim)) break;
             fence_after_sync();
             // Z has had its last reader: its rows take the output's
             uint8_t *zs = sm + st * LY::STAGE + LY::Z;
 #pragma unroll 1
-            for (int c = 0; c < D2; c += 32) {
-                float v[32];
-                tmem_ld32(tl + c, v);
+            for (int c = 0; c < D2; c += 16) {
+                float v[16];
+                tmem_ld16(tl + c, v);
                 tmem_wait_ld();
                 if (p.o_f32) {
                     const int t = t0 + row;
                     if (t < p.T && c < p.d2) {
                         float *o = (float *)p.o + (((long long)wk.b * p.T + t) * p.H + wk.h) * p.d2 + c;
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4)
+                        for (int k = 0; k < 16; k += 4)
                             *reinterpret_cast<float4 *>(o + k) = live ? make_float4(v[k], v[k + 1], v[k + 2], v[k + 3])
                                                                       : make_float4(0.f, 0.f, 0.f, 0.f);
                     }
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 8) {
+                    for (int k = 0; k < 16; k += 8) {
                         uint4 u = make_uint4(0, 0, 0, 0);
                         if (live)
                             u = make_uint4(bf16_pair(v[k], v[k + 1]), bf16_pair(v[k + 2], v[k + 3]),
@@ -552,6 +573,7 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
         }
         if (lane == 0) bulk_wait_all();
     } else if (warp < LY::YW0) {
+        setmaxnreg_inc<LY::RS>();
         // ---------------- the state: R^T[m][n] of row m = lane, half of the columns ----------------
         const int sw = warp - LY::SW0, q = sw & 3, half = sw >> 2, m = 32 * q + lane;
         constexpr int NC = D2 / 2;
@@ -567,7 +589,7 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
             if (i > 0) {
                 const float an = pw.at(wk.n(i - 1));
                 // the previous chunk's write, and (issued before it) the last read of the bf16 state
-                if (!mbar_wait(&ds_full, (uint32_t)((i - 1) & 1), status, lim)) break;
+                if (!mbar_wait_suspend(&ds_full, (uint32_t)((i - 1) & 1), status, lim)) break;
                 fence_after_sync();
                 if (32 * q < D1) {
 #pragma unroll
@@ -593,26 +615,28 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
             if (lane == 0) mbar_arrive(&s_ready);
         }
     } else {
+        setmaxnreg_dec<LY::RY>();
         // ---------------- Y times the write's weights ----------------
-        const int yt = tid - 32 * LY::YW0, q = warp & 3, m = 32 * q + lane;
+        const int yt = tid - 32 * LY::YW0, q = warp & 3, half = (warp - LY::YW0) >> 2, m = 32 * q + lane;
         static_assert(LY::YW0 % 4 == 0, "the warp's TMEM lanes");
         for (int i = 0; i < wk.nch; ++i) {
             const int st = i % NST, n = wk.n(i);
             uint8_t *s = sm + st * LY::STAGE;
-            if (!mbar_wait(&y_full[st], (uint32_t)((i / NST) & 1), status, lim)) break;
+            if (!mbar_wait_suspend(&y_full[st], (uint32_t)((i / NST) & 1), status, lim)) break;
             if (n < CT) {
-                if (!mbar_wait(&z_full[st], (uint32_t)((i / NST) & 1), status, lim)) break;
+                if (!mbar_wait_suspend(&z_full[st], (uint32_t)((i / NST) & 1), status, lim)) break;
                 zero_rows<D2>(s + LY::Z, n, yt, 32 * LY::YW);
                 fence_async_smem();
             }
             // (on the last chunk too, where nothing is written: without it a warp could arrive for this chunk
             // before another one has for the last, and complete that phase in its place)
-            if (i > 0 && !mbar_wait(&yp_free, (uint32_t)((i - 1) & 1), status, lim)) break;
+            if (i > 0 && !mbar_wait_suspend(&yp_free, (uint32_t)((i - 1) & 1), status, lim)) break;
             if (i + 1 < wk.nch) {  // (nobody reads the state behind the last chunk)
                 fence_after_sync();
                 if (32 * q < D1) {
 #pragma unroll 1
-                    for (int j0 = 0; j0 < CT; j0 += 32) weigh32<2>(s + LY::Y, m, pw.w, j0, n, taddr(tb, 32 * q, 0), LY::cY);
+                    for (int j0 = 64 * half; j0 < 64 * half + 64; j0 += kWeigh)
+                        weigh<2>(s + LY::Y, m, pw.w, j0, n, taddr(tb, 32 * q, 0), LY::cY);
                     tmem_wait_st();
                 }
             }
@@ -655,8 +679,18 @@ cudaError_t launch_one(const DecayPass &p, bool sum, cudaStream_t s) {
     const int bytes = sum ? (int)SumLayout<D1, D2>::BYTES : (int)PassLayout<D1, D2>::BYTES;
     const int threads = sum ? SumLayout<D1, D2>::THREADS : PassLayout<D1, D2>::THREADS;
     auto kern = sum ? decay_sum_tc_kernel<D1, D2> : decay_pass_tc_kernel<D1, D2>;
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    // once per device and kernel: the shared memory limit, and the register count that the shares rely on
+    static bool ready[2][64];
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
+    if (dev >= 64 || !ready[sum][dev]) {
+        if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return err;
+        cudaFuncAttributes attr;
+        if ((err = cudaFuncGetAttributes(&attr, kern)) != cudaSuccess) return err;
+        if (!sum && attr.numRegs * threads < PassLayout<D1, D2>::SHARES) return cudaErrorInvalidKernelImage;
+        if (dev < 64) ready[sum][dev] = true;
+    }
     launch_probe_mark(s);
     kern<<<dim3(p.nseg, p.H, p.B), threads, bytes, s>>>(p, maps);
     return cudaGetLastError();

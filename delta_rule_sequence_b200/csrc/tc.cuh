@@ -268,6 +268,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 // Stores of this thread's lane: N consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -293,20 +298,47 @@ __device__ __forceinline__ void tmem_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// NKS k-steps of 16 with the A operand in TMEM: lane = row, two consecutive k elements per 32-bit
-// column, so a k-step is 8 columns.
-template <int NKS, class OB>
-__device__ __forceinline__ void mma_steps_tmem_a(uint32_t d, uint32_t idesc, uint32_t a, uint64_t b, OB ob,
-                                                 bool accumulate) {
+// The same products issued by a whole warp in convergent code, one elected lane each: the descriptors then
+// stay in uniform registers.  From a single lane's branch every instruction first moves its operands there,
+// about 75 cycles an MMA whatever its width (measured on 128 x 64 and 128 x 128 tiles).
+template <int NKS, class OA, class OB>
+__device__ __forceinline__ void mma_steps_warp(uint32_t d, uint32_t idesc, uint64_t a, uint64_t b, OA oa, OB ob,
+                                               bool accumulate) {
 #pragma unroll
     for (int ks = 0; ks < NKS; ++ks)
         asm volatile(
-            "{\n\t.reg .pred p;\n\t"
+            "{\n\t.reg .pred p, q;\n\t"
+            "elect.sync _|q, 0xffffffff;\n\t"
             "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n"
             :
-            : "r"(d), "r"(a + 8 * ks), "l"(b + ob(ks)), "r"(idesc),
+            : "r"(d), "l"(a + oa(ks)), "l"(b + ob(ks)), "r"(idesc),
               "r"((accumulate || ks > 0) ? 1u : 0u));
+}
+// The A operand in TMEM: lane = row, two consecutive k elements per 32-bit column, so a k-step is 8
+// columns; step ks starts at column oa(ks).
+template <int NKS, class OA, class OB>
+__device__ __forceinline__ void mma_steps_tmem_a_warp(uint32_t d, uint32_t idesc, uint32_t a, uint64_t b, OA oa, OB ob,
+                                                      bool accumulate) {
+#pragma unroll
+    for (int ks = 0; ks < NKS; ++ks)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t"
+            "elect.sync _|q, 0xffffffff;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
+            :
+            : "r"(d), "r"(a + (uint32_t)oa(ks)), "l"(b + ob(ks)), "r"(idesc),
+              "r"((accumulate || ks > 0) ? 1u : 0u));
+}
+__device__ __forceinline__ void mma_commit_warp(uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n"
+        :
+        : "r"(smem_u32(bar))
+        : "memory");
 }
 
 __device__ __forceinline__ void tmem_wait_ld() {
@@ -392,6 +424,31 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint32
     record_status(status, PRISM_ERR_TIMEOUT);
     return false;
 }
+
+// The same wait with a hint to suspend for up to kSuspendNs per poll: a waiting warp then takes no issue
+// slots from the warps that it waits for.
+constexpr uint32_t kSuspendNs = 20000;
+__device__ __forceinline__ bool mbar_wait_suspend(uint64_t *bar, uint32_t parity, uint32_t *status, uint32_t limit) {
+    for (uint32_t i = 0; i < limit; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendNs)
+            : "memory");
+        if (ok) return true;
+    }
+    record_status(status, PRISM_ERR_TIMEOUT);
+    return false;
+}
+
+// Registers of each of the executing warpgroup's threads from here on (all four warps execute it).
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // bf16 pack of two floats (round to nearest even), low half = a.
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
