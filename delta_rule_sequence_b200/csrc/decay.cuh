@@ -61,38 +61,86 @@ __device__ __forceinline__ int decay_len(const int *lengths, int b, int T) {
     return n < 0 ? 0 : (n > T ? T : n);
 }
 
-// a^n for a whole n >= 0 (0^0 = 1), computed in 64 bits: with a near 1 and n in the thousands a
-// 32-bit log would lose the last digits of the power.
+// a^n for a whole n >= 0 (0^0 = 1), by squaring in 64 bits: with a near 1 and n in the thousands 32 bits would
+// lose the last digits of the power.  (exp2(n log2 a) in 64 bits took 1.5 us of a CTA's start.)
 __device__ __forceinline__ float decay_pow(float a, int n) {
-    if (n == 0) return 1.f;
-    if (a == 0.f) return 0.f;
-    return (float)exp2((double)n * log2((double)a));
+    double r = 1.0, s = (double)a;
+    for (; n > 0; n >>= 1, s *= s)
+        if (n & 1) r *= s;
+    return (float)r;
 }
+
+// Dependent launches: a kernel lets the next one of the call start once it has itself seen its predecessor
+// complete, so whatever a kernel reads before decay_wait() is older than the call.
+__device__ __forceinline__ void decay_wait() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Launches `kern` so that its start may overlap the end of the call's previous kernel (`dependent`).
+template <typename... P, typename... A>
+cudaError_t decay_launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, bool dependent, const A &...args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = dependent ? 1 : 0;
+    launch_probe_mark(s);
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// Passes (or segment sums) of one launch, all of the same B, H, T, lengths and segments: the CTAs of one
+// after those of the other, grid {count * nseg, H, B}.
+constexpr int kDecaySet = 3;
+struct DecayPassSet {
+    int count;
+    bool dependent;  // not the first kernel of its call
+    DecayPass p[kDecaySet];
+};
+
+// Width that a kernel is built for.
+inline int decay_padded(int d) { return d <= 64 ? 64 : 128; }
 
 constexpr int kDecayChunkSimt = 64, kDecayChunkTc = 128;  // tokens of a chunk
 
 // fp32 operands, on CUDA cores; bf16 operands, on the tensor cores.
-cudaError_t launch_decay_sum_simt(const DecayPass &p, cudaStream_t s);
-cudaError_t launch_decay_pass_simt(const DecayPass &p, cudaStream_t s);
-cudaError_t launch_decay_sum_tc(const DecayPass &p, cudaStream_t s);
-cudaError_t launch_decay_pass_tc(const DecayPass &p, cudaStream_t s);
+// Every pass of a set has the same padded widths (decay_padded).
+cudaError_t launch_decay_simt(const DecayPassSet &set, bool sum, cudaStream_t s);
+cudaError_t launch_decay_tc(const DecayPassSet &set, bool sum, cudaStream_t s);
 cudaError_t decay_status(uint32_t *out);  // read and clear the tensor-core kernels' status word
 
 // Entry states of every segment from the segments' sums, in place of them, and the exit state.
-struct DecayCarry {
-    int BH, H, T, elems;      // elems = d1 * d2
-    int nseg, seg_tokens, reverse;
-    const float *decay;
-    const int *lengths;
+struct DecayCarryOne {
+    int reverse;
     const float *init;        // [BH][elems] or null (zero)
     float *F;                 // [BH][nseg][elems]: sums in, entry states out
     float *final_state;       // [BH][elems] or null
 };
+struct DecayCarry {
+    int BH, H, T, elems;      // elems = d1 * d2
+    int nseg, seg_tokens;
+    const float *decay;
+    const int *lengths;
+    int count;
+    bool dependent;
+    DecayCarryOne c[2];
+};
 cudaError_t launch_decay_carry(const DecayCarry &c, cudaStream_t s);
 
-// out[b,t,g,:] = sum over the `div` heads of group g of part[b,t,g*div + i,:] (fp32 -> io).
-cudaError_t launch_decay_group_sum(const float *part, void *out, long long rows, int groups, int div, int d,
-                                   bool io_f32, cudaStream_t s);
+// out[b,t,g,:] = sum over the `div` heads of group g of part[b,t,g*div + i,:] (fp32 -> io), for dk and dv.
+struct DecayGroupSum {
+    long long groups;         // B * T * Hkv
+    int div;
+    const float *part[2];
+    void *out[2];
+    int d[2];
+};
+cudaError_t launch_decay_group_sum(const DecayGroupSum &g, bool io_f32, cudaStream_t s);
 
 cudaError_t launch_decay_step(int B, int H, int dk, int dv, const DecayTensor &q, const DecayTensor &k,
                               const DecayTensor &v, const float *decay, float *S, void *o, bool io_f32,

@@ -1,6 +1,7 @@
 // decay_api.cu -- the C entry points of the decay scan: argument checks, the segment plan, the launches.
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "api.cuh"
 #include "decay.cuh"
@@ -66,23 +67,24 @@ prism_status check_call(const prism_decay_shape *s, const void *q, const void *k
     return PRISM_OK;
 }
 
-// Segments per sequence.  One CTA per SM walks one segment, chunk after chunk, so a plan's time is about
-// (waves of CTAs) x (chunks of a segment + what starting one costs, about kStart chunks).
+// Segments per sequence, for a launch of `passes` passes.  One CTA per SM walks one segment, chunk after
+// chunk, so a plan's time is about (waves of CTAs) x (chunks of a segment + what starting one costs, about
+// kStart chunks).
 struct DecayPlan {
     int chunk, nseg, seg_tokens;
 };
 constexpr int kStart = 2;
 
-DecayPlan plan_of(const prism_decay_shape &s) {
+DecayPlan plan_of(const prism_decay_shape &s, int passes) {
     const int chunk = s.io == PRISM_F32 ? kDecayChunkSimt : kDecayChunkTc;
     const int nch = std::max(1, (s.T + chunk - 1) / chunk);
-    const long long bh = std::max(1LL, (long long)s.B * s.H);
+    const long long ctas = std::max(1LL, (long long)s.B * s.H * passes);
     const int sms = sm_count();
     DecayPlan best{chunk, 1, nch * chunk};
     long long least = 0;
     for (int want = 1; want <= std::min(nch, 128); ++want) {
         const int per = (nch + want - 1) / want, nseg = (nch + per - 1) / per;
-        const long long cost = (bh * nseg + sms - 1) / sms * (per + kStart);
+        const long long cost = (ctas * nseg + sms - 1) / sms * (per + kStart);
         if (want == 1 || cost < least) {
             least = cost;
             best = DecayPlan{chunk, nseg, per * chunk};
@@ -97,10 +99,10 @@ size_t sums_bytes(const prism_decay_shape &s, const DecayPlan &pl) {
     return align256((size_t)s.B * s.H * pl.nseg * s.dk * s.dv * 4);
 }
 
-// fp32 gradients of one operand per query head, where heads share keys and values.
-size_t shared_grad_bytes(const prism_decay_shape &s) {
+// fp32 gradients of k or v (width d) per query head, where heads share keys and values.
+size_t shared_grad_bytes(const prism_decay_shape &s, int d) {
     if (s.H == 0 || s.Hkv == s.H) return 0;
-    return align256((size_t)s.B * s.T * s.H * std::max(s.dk, s.dv) * 4);
+    return align256((size_t)s.B * s.T * s.H * d * 4);
 }
 
 DecayTensor dense(const prism_decay_shape &s, const void *p, int d) {
@@ -114,32 +116,47 @@ struct Runner {
     const int *lengths;
     cudaStream_t stream;
     cudaError_t err = cudaSuccess;
+    bool launched = false;  // a kernel of this call is in the stream
 
     bool f32() const { return s.io == PRISM_F32; }
-    void sum(const DecayTensor &y, const DecayTensor &z, int d1, int d2, bool reverse, float *F) {
-        if (err != cudaSuccess) return;
+    DecayPass common(int d1, int d2, bool reverse) const {
         DecayPass p{};
         p.B = s.B; p.H = s.H; p.T = s.T; p.d1 = d1; p.d2 = d2;
-        p.y = y; p.z = z; p.decay = decay; p.lengths = lengths;
-        p.F = F; p.reverse = reverse; p.nseg = pl.nseg; p.seg_tokens = pl.seg_tokens;
-        p.stall = (debug_flags() & kDebugStallDecay) != 0;
-        err = f32() ? launch_decay_sum_simt(p, stream) : launch_decay_sum_tc(p, stream);
-    }
-    void carry(float *F, const float *init, float *final_state, bool reverse) {
-        if (err != cudaSuccess) return;
-        DecayCarry c{s.B * s.H, s.H, s.T, s.dk * s.dv, pl.nseg, pl.seg_tokens, reverse ? 1 : 0, decay, lengths, init, F, final_state};
-        err = launch_decay_carry(c, stream);
-    }
-    void pass(const DecayTensor &x, const DecayTensor &y, const DecayTensor &z, int d1, int d2, const float *entry,
-              bool entry_t, bool reverse, void *o, bool o_f32) {
-        if (err != cudaSuccess) return;
-        DecayPass p{};
-        p.B = s.B; p.H = s.H; p.T = s.T; p.d1 = d1; p.d2 = d2;
-        p.x = x; p.y = y; p.z = z; p.decay = decay; p.lengths = lengths;
-        p.entry = entry; p.entry_t = entry_t; p.reverse = reverse; p.o = o; p.o_f32 = o_f32;
+        p.decay = decay; p.lengths = lengths; p.reverse = reverse;
         p.nseg = pl.nseg; p.seg_tokens = pl.seg_tokens;
         p.stall = (debug_flags() & kDebugStallDecay) != 0;
-        err = f32() ? launch_decay_pass_simt(p, stream) : launch_decay_pass_tc(p, stream);
+        return p;
+    }
+    DecayPass sum(const DecayTensor &y, const DecayTensor &z, int d1, int d2, bool reverse, float *F) const {
+        DecayPass p = common(d1, d2, reverse);
+        p.y = y; p.z = z; p.F = F;
+        return p;
+    }
+    DecayPass pass(const DecayTensor &x, const DecayTensor &y, const DecayTensor &z, int d1, int d2, const float *entry,
+                   bool entry_t, bool reverse, void *o, bool o_f32) const {
+        DecayPass p = common(d1, d2, reverse);
+        p.x = x; p.y = y; p.z = z; p.entry = entry; p.entry_t = entry_t; p.o = o; p.o_f32 = o_f32;
+        return p;
+    }
+    // one launch for neighbours of the same padded widths
+    void run(std::initializer_list<DecayPass> list, bool sum) {
+        DecayPassSet set{};
+        for (const DecayPass *p = list.begin(); p != list.end(); ++p) {
+            set.p[set.count++] = *p;
+            const bool more = p + 1 != list.end() && decay_padded(p[1].d1) == decay_padded(p->d1) &&
+                              decay_padded(p[1].d2) == decay_padded(p->d2);
+            if (more && set.count < kDecaySet) continue;
+            set.dependent = launched;
+            launched = true;
+            if (err == cudaSuccess) err = f32() ? launch_decay_simt(set, sum, stream) : launch_decay_tc(set, sum, stream);
+            set.count = 0;
+        }
+    }
+    void carry(std::initializer_list<DecayCarryOne> list) {
+        DecayCarry c{s.B * s.H, s.H, s.T, s.dk * s.dv, pl.nseg, pl.seg_tokens, decay, lengths, 0, launched, {}};
+        launched = true;
+        for (const DecayCarryOne &o : list) c.c[c.count++] = o;
+        if (err == cudaSuccess) err = launch_decay_carry(c, stream);
     }
     // a state without tokens: out = init or zero
     void copy_state(float *out, const float *init) {
@@ -160,7 +177,7 @@ prism_status prism_decay_scan_fwd_workspace_size(const prism_decay_shape *shape,
     if (!bytes) return PRISM_ERR_INVALID_ARG;
     const prism_status st = check_shape(shape);
     if (st != PRISM_OK) return st;
-    *bytes = std::max<size_t>(256, sums_bytes(*shape, plan_of(*shape)));
+    *bytes = std::max<size_t>(256, sums_bytes(*shape, plan_of(*shape, 1)));
     return PRISM_OK;
 }
 
@@ -182,17 +199,17 @@ prism_status prism_decay_scan_fwd(const prism_decay_shape *shape, const void *q,
                          {lengths, (size_t)s.B * 4}, {S_final == S0 ? nullptr : S0, state}};
     if (c.work && outputs_alias(outs, 3, ins, 6)) return PRISM_ERR_INVALID_ARG;
     if (s.B == 0 || s.H == 0) return PRISM_OK;
-    Runner r{s, plan_of(s), decay, lengths, (cudaStream_t)stream};
+    Runner r{s, plan_of(s, 1), decay, lengths, (cudaStream_t)stream};
     float *F = (float *)workspace;
     if (s.T == 0) {
         r.copy_state(S_final, S0);
     } else {
         const bool cut = r.pl.nseg > 1;
-        if (cut || S_final) r.sum(c.k.t, c.v.t, s.dk, s.dv, false, F);
-        if (cut) r.carry(F, S0, S_final, false);
-        r.pass(c.q.t, c.k.t, c.v.t, s.dk, s.dv, cut ? F : S0, false, false, o, s.io == PRISM_F32);
+        if (cut || S_final) r.run({r.sum(c.k.t, c.v.t, s.dk, s.dv, false, F)}, true);
+        if (cut) r.carry({{0, S0, F, S_final}});
+        r.run({r.pass(c.q.t, c.k.t, c.v.t, s.dk, s.dv, cut ? F : S0, false, false, o, s.io == PRISM_F32)}, false);
         // after the pass, which reads S0: S_final may be S0
-        if (!cut && S_final) r.carry(F, S0, S_final, false);
+        if (!cut && S_final) r.carry({{0, S0, F, S_final}});
     }
     probe_finish((cudaStream_t)stream);
     return cuda_status(r.err);
@@ -202,7 +219,8 @@ prism_status prism_decay_scan_bwd_workspace_size(const prism_decay_shape *shape,
     if (!bytes) return PRISM_ERR_INVALID_ARG;
     const prism_status st = check_shape(shape);
     if (st != PRISM_OK) return st;
-    *bytes = std::max<size_t>(256, 2 * sums_bytes(*shape, plan_of(*shape)) + shared_grad_bytes(*shape));
+    *bytes = std::max<size_t>(256, 2 * sums_bytes(*shape, plan_of(*shape, 3)) + shared_grad_bytes(*shape, shape->dk) +
+                                       shared_grad_bytes(*shape, shape->dv));
     return PRISM_OK;
 }
 
@@ -228,31 +246,32 @@ prism_status prism_decay_scan_bwd(const prism_decay_shape *shape, const void *q,
                          {S0, state}, {dO, rows * s.H * s.dv}, {dS_final, state}};
     if (c.work && outputs_alias(outs, 5, ins, 8)) return PRISM_ERR_INVALID_ARG;
     if (s.B == 0 || s.H == 0) return PRISM_OK;
-    Runner r{s, plan_of(s), decay, lengths, (cudaStream_t)stream};
+    Runner r{s, plan_of(s, 3), decay, lengths, (cudaStream_t)stream};
     if (s.T == 0) {
         r.copy_state(dS0, dS_final);
     } else {
         const bool cut = r.pl.nseg > 1, f32 = s.io == PRISM_F32, shared = s.Hkv != s.H;
         const size_t sb = sums_bytes(s, r.pl);
-        float *FS = (float *)workspace, *FG = (float *)((char *)workspace + sb), *part = (float *)((char *)workspace + 2 * sb);
+        char *ws = (char *)workspace;
+        float *FS = (float *)ws, *FG = (float *)(ws + sb), *dk_part = (float *)(ws + 2 * sb),
+              *dv_part = (float *)(ws + 2 * sb + shared_grad_bytes(s, s.dk));
         const DecayTensor g = dense(s, dO, s.dv);
-        const long long tokens = (long long)s.B * s.T;
+        const DecayPass sum_S = r.sum(c.k.t, c.v.t, s.dk, s.dv, false, FS), sum_G = r.sum(c.q.t, g, s.dk, s.dv, true, FG);
         if (cut) {
-            r.sum(c.k.t, c.v.t, s.dk, s.dv, false, FS);
-            r.carry(FS, S0, nullptr, false);
-        }
-        if (cut || dS0) {
-            r.sum(c.q.t, g, s.dk, s.dv, true, FG);
-            r.carry(FG, dS_final, dS0, true);
+            r.run({sum_S, sum_G}, true);
+            r.carry({{0, S0, FS, nullptr}, {1, dS_final, FG, dS0}});
+        } else if (dS0) {
+            r.run({sum_G}, true);
+            r.carry({{1, dS_final, FG, dS0}});
         }
         const float *ES = cut ? FS : S0, *EG = cut ? FG : dS_final;
-        r.pass(g, c.v.t, c.k.t, s.dv, s.dk, ES, true, false, dq, f32);
-        r.pass(c.v.t, g, c.q.t, s.dv, s.dk, EG, true, true, shared ? part : dk, shared || f32);
+        r.run({r.pass(g, c.v.t, c.k.t, s.dv, s.dk, ES, true, false, dq, f32),
+               r.pass(c.v.t, g, c.q.t, s.dv, s.dk, EG, true, true, shared ? dk_part : dk, shared || f32),
+               r.pass(c.k.t, c.q.t, g, s.dk, s.dv, EG, false, true, shared ? dv_part : dv, shared || f32)},
+              false);
         if (shared && r.err == cudaSuccess)
-            r.err = launch_decay_group_sum(part, dk, tokens, s.Hkv, s.H / s.Hkv, s.dk, f32, r.stream);
-        r.pass(c.k.t, c.q.t, g, s.dk, s.dv, EG, false, true, shared ? part : dv, shared || f32);
-        if (shared && r.err == cudaSuccess)
-            r.err = launch_decay_group_sum(part, dv, tokens, s.Hkv, s.H / s.Hkv, s.dv, f32, r.stream);
+            r.err = launch_decay_group_sum({(long long)s.B * s.T * s.Hkv, s.H / s.Hkv, {dk_part, dv_part}, {dk, dv}, {s.dk, s.dv}},
+                                           f32, r.stream);
     }
     probe_finish((cudaStream_t)stream);
     return cuda_status(r.err);

@@ -55,10 +55,12 @@ __device__ __forceinline__ int write_exponent(int j, int n, int reverse) { retur
 
 // F[n][m] of one segment: the state that its tokens alone leave behind.
 template <int D1, int D2>
-__global__ void __launch_bounds__(NT) decay_sum_simt_kernel(DecayPass p) {
+__global__ void __launch_bounds__(NT) decay_sum_simt_kernel(const __grid_constant__ DecayPassSet set) {
     extern __shared__ __align__(16) float sm[];
     float *Y = sm, *Z = Y + CH * (D1 + 4), *pw = Z + CH * (D2 + 4), *w = pw + CH + 1;
-    const int seg = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    decay_wait();
+    const DecayPass &p = set.p[blockIdx.x / set.p[0].nseg];
+    const int seg = blockIdx.x % p.nseg, h = blockIdx.y, b = blockIdx.z;
     const int len = decay_len(p.lengths, b, p.T);
     const int s0 = seg * p.seg_tokens;
     const int s1 = min(s0 + p.seg_tokens, len);
@@ -97,12 +99,14 @@ __global__ void __launch_bounds__(NT) decay_sum_simt_kernel(DecayPass p) {
 // One segment's outputs, chunk by chunk, the state in shared memory (R^T: rows along y, so that the
 // entry term X R^T reads like the P Z product).
 template <int D1, int D2>
-__global__ void __launch_bounds__(NT) decay_pass_simt_kernel(DecayPass p) {
+__global__ void __launch_bounds__(NT) decay_pass_simt_kernel(const __grid_constant__ DecayPassSet set) {
     extern __shared__ __align__(16) float sm[];
     constexpr int PP = CH + 4;
     float *X = sm, *Y = X + CH * (D1 + 4), *Z = Y + CH * (D1 + 4), *R = Z + CH * (D2 + 4), *P = R + D1 * (D2 + 4),
           *pw = P + CH * PP, *w = pw + CH + 1;
-    const int seg = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    decay_wait();
+    const DecayPass &p = set.p[blockIdx.x / set.p[0].nseg];
+    const int seg = blockIdx.x % p.nseg, h = blockIdx.y, b = blockIdx.z;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int len = decay_len(p.lengths, b, p.T);
     const int s0 = seg * p.seg_tokens;
@@ -233,20 +237,14 @@ __global__ void __launch_bounds__(NT) decay_pass_simt_kernel(DecayPass p) {
 }
 
 template <int D1, int D2>
-cudaError_t launch_one(const DecayPass &p, bool sum, cudaStream_t s) {
+cudaError_t launch_one(const DecayPassSet &set, bool sum, cudaStream_t s) {
+    const DecayPass &p = set.p[0];
     const int tiles = CH * (D1 + 4) + CH * (D2 + 4) + CH + 1 + CH;
     const int bytes = 4 * (sum ? tiles : tiles + CH * (D1 + 4) + D1 * (D2 + 4) + CH * (CH + 4));
     auto kern = sum ? decay_sum_simt_kernel<D1, D2> : decay_pass_simt_kernel<D1, D2>;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (err != cudaSuccess) return err;
-    launch_probe_mark(s);
-    kern<<<dim3(p.nseg, p.H, p.B), NT, bytes, s>>>(p);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_widths(const DecayPass &p, bool sum, cudaStream_t s) {
-    if (p.d1 <= 64) return p.d2 <= 64 ? launch_one<64, 64>(p, sum, s) : launch_one<64, 128>(p, sum, s);
-    return p.d2 <= 64 ? launch_one<128, 64>(p, sum, s) : launch_one<128, 128>(p, sum, s);
+    return decay_launch(kern, dim3(set.count * p.nseg, p.H, p.B), NT, bytes, s, set.dependent, set);
 }
 
 // Four state elements per thread, walked over the segments in order: entry states replace the sums.  The
@@ -255,7 +253,9 @@ cudaError_t launch_widths(const DecayPass &p, bool sum, cudaStream_t s) {
 // thread they were the kernel's time (32 us instead of 6 for 16 heads of 65536 tokens).
 constexpr int kAhead = 8;
 
-__global__ void __launch_bounds__(128) decay_carry_kernel(DecayCarry c) {
+__global__ void __launch_bounds__(128) decay_carry_kernel(const __grid_constant__ DecayCarry c) {
+    decay_wait();
+    const DecayCarryOne &o = c.c[blockIdx.z];
     __shared__ float pw[2];
     const int bh = blockIdx.x, e = 4 * (blockIdx.y * 128 + threadIdx.x);
     const int len = decay_len(c.lengths, bh / c.H, c.T);
@@ -263,19 +263,19 @@ __global__ void __launch_bounds__(128) decay_carry_kernel(DecayCarry c) {
     if (threadIdx.x < 2) pw[threadIdx.x] = decay_pow(c.decay[bh % c.H], threadIdx.x == 0 ? c.seg_tokens : rest);
     __syncthreads();
     if (e >= c.elems) return;
-    float4 *F = reinterpret_cast<float4 *>(c.F + (long long)bh * c.nseg * c.elems + e);
+    float4 *F = reinterpret_cast<float4 *>(o.F + (long long)bh * c.nseg * c.elems + e);
     const long long step = c.elems / 4;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (c.init) s = *reinterpret_cast<const float4 *>(c.init + (long long)bh * c.elems + e);
+    if (o.init) s = *reinterpret_cast<const float4 *>(o.init + (long long)bh * c.elems + e);
     for (int i0 = 0; i0 < c.nseg; i0 += kAhead) {
         float4 f[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
-            if (i0 + k < c.nseg) f[k] = F[(c.reverse ? c.nseg - 1 - i0 - k : i0 + k) * step];
+            if (i0 + k < c.nseg) f[k] = F[(o.reverse ? c.nseg - 1 - i0 - k : i0 + k) * step];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             if (i0 + k >= c.nseg) break;
-            const int seg = c.reverse ? c.nseg - 1 - i0 - k : i0 + k;
+            const int seg = o.reverse ? c.nseg - 1 - i0 - k : i0 + k;
             F[seg * step] = s;
             if (seg < last || (seg == last && rest > 0)) {
                 const float a = pw[seg == last];
@@ -283,13 +283,17 @@ __global__ void __launch_bounds__(128) decay_carry_kernel(DecayCarry c) {
             }
         }
     }
-    if (c.final_state) *reinterpret_cast<float4 *>(c.final_state + (long long)bh * c.elems + e) = s;
+    if (o.final_state) *reinterpret_cast<float4 *>(o.final_state + (long long)bh * c.elems + e) = s;
 }
 
 template <typename IO>
-__global__ void decay_group_sum_kernel(const float *part, IO *out, long long total, int div, int d) {
-    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;  // over [rows * groups, d / 4]
-    if (i >= total) return;
+__global__ void decay_group_sum_kernel(DecayGroupSum a) {
+    decay_wait();
+    const int which = blockIdx.y, d = a.d[which], div = a.div;
+    const float *part = a.part[which];
+    IO *out = (IO *)a.out[which];
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;  // over [groups, d / 4]
+    if (i >= a.groups * (d / 4)) return;
     const long long g = i / (d / 4);
     const int c = (int)(i % (d / 4)) * 4;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -305,23 +309,20 @@ __global__ void decay_group_sum_kernel(const float *part, IO *out, long long tot
 
 }  // namespace
 
-cudaError_t launch_decay_sum_simt(const DecayPass &p, cudaStream_t s) { return launch_widths(p, true, s); }
-cudaError_t launch_decay_pass_simt(const DecayPass &p, cudaStream_t s) { return launch_widths(p, false, s); }
-
-cudaError_t launch_decay_carry(const DecayCarry &c, cudaStream_t s) {
-    launch_probe_mark(s);
-    decay_carry_kernel<<<dim3(c.BH, (c.elems + 511) / 512), 128, 0, s>>>(c);
-    return cudaGetLastError();
+cudaError_t launch_decay_simt(const DecayPassSet &set, bool sum, cudaStream_t s) {
+    const int d1 = decay_padded(set.p[0].d1), d2 = decay_padded(set.p[0].d2);
+    if (d1 == 64) return d2 == 64 ? launch_one<64, 64>(set, sum, s) : launch_one<64, 128>(set, sum, s);
+    return d2 == 64 ? launch_one<128, 64>(set, sum, s) : launch_one<128, 128>(set, sum, s);
 }
 
-cudaError_t launch_decay_group_sum(const float *part, void *out, long long rows, int groups, int div, int d,
-                                   bool io_f32, cudaStream_t s) {
-    const long long total = rows * groups * (d / 4);
-    const unsigned blocks = (unsigned)((total + 255) / 256);
-    launch_probe_mark(s);
-    if (io_f32) decay_group_sum_kernel<float><<<blocks, 256, 0, s>>>(part, (float *)out, total, div, d);
-    else decay_group_sum_kernel<__nv_bfloat16><<<blocks, 256, 0, s>>>(part, (__nv_bfloat16 *)out, total, div, d);
-    return cudaGetLastError();
+cudaError_t launch_decay_carry(const DecayCarry &c, cudaStream_t s) {
+    return decay_launch(decay_carry_kernel, dim3(c.BH, (c.elems + 511) / 512, c.count), 128, 0, s, c.dependent, c);
+}
+
+cudaError_t launch_decay_group_sum(const DecayGroupSum &g, bool io_f32, cudaStream_t s) {
+    const int d = g.d[0] > g.d[1] ? g.d[0] : g.d[1];
+    const dim3 grid((unsigned)((g.groups * (d / 4) + 255) / 256), 2);
+    return decay_launch(io_f32 ? decay_group_sum_kernel<float> : decay_group_sum_kernel<__nv_bfloat16>, grid, 256, 0, s, true, g);
 }
 
 }  // namespace prism

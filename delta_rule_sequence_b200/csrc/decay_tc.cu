@@ -36,6 +36,9 @@ __device__ uint32_t g_decay_status;
 struct DecayMaps {
     CUtensorMap x, y, z, o;
 };
+struct DecayMapSet {
+    DecayMaps m[kDecaySet];
+};
 
 // Bytes of a tile of 128 tokens, D columns (64-column blocks of 128 rows x 128 bytes).
 constexpr uint32_t kBlk = CT * 128;
@@ -47,7 +50,7 @@ constexpr uint32_t tile_bytes() { return kBlk * (D / 64); }
 struct Walk {
     int b, h, seg, len, s0, s1, send, nch, reverse;
     __device__ explicit Walk(const DecayPass &p) {
-        seg = blockIdx.x;
+        seg = blockIdx.x % p.nseg;
         h = blockIdx.y;
         b = blockIdx.z;
         len = decay_len(p.lengths, b, p.T);
@@ -153,7 +156,9 @@ struct SumLayout {
 
 template <int D1, int D2>
 __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
-    decay_sum_tc_kernel(DecayPass p, const __grid_constant__ DecayMaps maps) {
+    decay_sum_tc_kernel(const __grid_constant__ DecayPassSet set, const __grid_constant__ DecayMapSet map_set) {
+    const DecayPass &p = set.p[blockIdx.x / set.p[0].nseg];
+    const DecayMaps &maps = map_set.m[blockIdx.x / set.p[0].nseg];
     using LY = SumLayout<D1, D2>;
     constexpr int NST = LY::NST;
     extern __shared__ uint8_t smem_raw[];
@@ -163,6 +168,7 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
     __shared__ __align__(16) float w_last[CT];  // the weights of the walk's last chunk
     __shared__ uint32_t tmem_base_sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    decay_wait();
     const Walk wk(p);
     uint32_t *status = &g_decay_status;
     const uint32_t lim = p.stall ? kStallPolls : kPolls;
@@ -327,7 +333,9 @@ struct PassLayout {
 
 template <int D1, int D2>
 __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
-    decay_pass_tc_kernel(DecayPass p, const __grid_constant__ DecayMaps maps) {
+    decay_pass_tc_kernel(const __grid_constant__ DecayPassSet set, const __grid_constant__ DecayMapSet map_set) {
+    const DecayPass &p = set.p[blockIdx.x / set.p[0].nseg];
+    const DecayMaps &maps = map_set.m[blockIdx.x / set.p[0].nseg];
     using LY = PassLayout<D1, D2>;
     constexpr int NST = LY::NST;
     extern __shared__ uint8_t smem_raw[];
@@ -529,23 +537,40 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
             if (lane == 0) mbar_arrive(&o_scaled);
             if (!mbar_wait_suspend(&o_full, (uint32_t)(i & 1), status, lim)) break;
             fence_after_sync();
-            // Z has had its last reader: its rows take the output's
+            // Z has had its last reader: its rows take the output's, as bf16, or (shared heads' gradients) as fp32,
+            // 32 columns at a time; rows behind the sequence's end are zeros
             uint8_t *zs = sm + st * LY::STAGE + LY::Z;
+            if (p.o_f32) {
+                uint8_t *box = zs + q * 4096;
 #pragma unroll 1
-            for (int c = 0; c < D2; c += 16) {
-                float v[16];
-                tmem_ld16(tl + c, v);
-                tmem_wait_ld();
-                if (p.o_f32) {
-                    const int t = t0 + row;
-                    if (t < p.T && c < p.d2) {
-                        float *o = (float *)p.o + (((long long)wk.b * p.T + t) * p.H + wk.h) * p.d2 + c;
+                for (int c = 0; c < D2 && c < p.d2; c += 32) {
+                    if (c > 0) {
+                        if (lane == 0) bulk_wait_read();
+                        __syncwarp();
+                    }
+#pragma unroll
+                    for (int c16 = 0; c16 < 32; c16 += 16) {
+                        float v[16];
+                        tmem_ld16(tl + c + c16, v);
+                        tmem_wait_ld();
 #pragma unroll
                         for (int k = 0; k < 16; k += 4)
-                            *reinterpret_cast<float4 *>(o + k) = live ? make_float4(v[k], v[k + 1], v[k + 2], v[k + 3])
-                                                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+                            *reinterpret_cast<float4 *>(box + lane * 128 + ((((c16 + k) >> 2) ^ (lane & 7)) << 4)) =
+                                live ? make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
                     }
-                } else {
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_4d(&maps.o, box, c, wk.h, t0 + 32 * q, wk.b);
+                        bulk_commit();
+                    }
+                }
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < D2; c += 16) {
+                    float v[16];
+                    tmem_ld16(tl + c, v);
+                    tmem_wait_ld();
 #pragma unroll
                     for (int k = 0; k < 16; k += 8) {
                         uint4 u = make_uint4(0, 0, 0, 0);
@@ -555,19 +580,20 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
                         *reinterpret_cast<uint4 *>(zs + sw128_off(row, c + k, kBlk)) = u;
                     }
                 }
-            }
-            fence_before_sync();
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&o_free);
-                if (!p.o_f32) {
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
 #pragma unroll
                     for (int c = 0; c < D2 / 64; ++c)
                         if (64 * c < p.d2) tma_store_4d(&maps.o, zs + c * kBlk + 32 * q * 128, 64 * c, wk.h, t0 + 32 * q, wk.b);
                     bulk_commit();
-                    bulk_wait_read();
                 }
+            }
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&o_free);
+                bulk_wait_read();
                 mbar_arrive(&z_free[st]);
             }
         }
@@ -578,12 +604,23 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
         const int sw = warp - LY::SW0, q = sw & 3, half = sw >> 2, m = 32 * q + lane;
         constexpr int NC = D2 / 2;
         float r[NC];
+        // (the entry state comes from the call's previous kernel; the other roles' inputs are older than the call)
+        decay_wait();
         const float *E = p.entry && m < p.d1
                              ? p.entry + (((long long)wk.b * p.H + wk.h) * p.nseg + wk.seg) * p.d1 * p.d2 : nullptr;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const int nn = half * NC + c;
-            r[c] = E && nn < p.d2 ? (p.entry_t ? E[m * p.d2 + nn] : E[nn * p.d1 + m]) : 0.f;
+        for (int c = 0; c < NC; c += 4) {
+            const int nn = half * NC + c;  // (d2 is a multiple of 4)
+            if (E && nn < p.d2 && p.entry_t) {
+                const float4 e = *reinterpret_cast<const float4 *>(E + m * p.d2 + nn);
+                r[c] = e.x;
+                r[c + 1] = e.y;
+                r[c + 2] = e.z;
+                r[c + 3] = e.w;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) r[c + k] = E && nn < p.d2 ? E[(nn + k) * p.d1 + m] : 0.f;
+            }
         }
         for (int i = 0; i < wk.nch; ++i) {
             if (i > 0) {
@@ -663,19 +700,23 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
 }
 
 bool operand_map(CUtensorMap *m, const DecayPass &p, const DecayTensor &t, int d) {
-    return bf16_rows_map(m, t.p, p.B, p.T, p.H / t.div, d, t.sb, t.st, t.sh, CT);
+    return rows_map(m, t.p, false, p.B, p.T, p.H / t.div, d, t.sb, t.st, t.sh, CT);
 }
 
 template <int D1, int D2>
-cudaError_t launch_one(const DecayPass &p, bool sum, cudaStream_t s) {
-    DecayMaps maps;
-    bool ok = operand_map(&maps.y, p, p.y, p.d1) && operand_map(&maps.z, p, p.z, p.d2);
-    if (!sum) {
-        ok = ok && operand_map(&maps.x, p, p.x, p.d1);
-        if (!p.o_f32)
-            ok = ok && bf16_rows_map(&maps.o, p.o, p.B, p.T, p.H, p.d2, (long long)p.T * p.H * p.d2, (long long)p.H * p.d2, p.d2, 32);
+cudaError_t launch_one(const DecayPassSet &set, bool sum, cudaStream_t s) {
+    DecayMapSet maps;
+    for (int i = 0; i < set.count; ++i) {
+        const DecayPass &p = set.p[i];
+        DecayMaps &m = maps.m[i];
+        bool ok = operand_map(&m.y, p, p.y, p.d1) && operand_map(&m.z, p, p.z, p.d2);
+        if (!sum) {
+            ok = ok && operand_map(&m.x, p, p.x, p.d1);
+            ok = ok && rows_map(&m.o, p.o, p.o_f32, p.B, p.T, p.H, p.d2, (long long)p.T * p.H * p.d2, (long long)p.H * p.d2, p.d2, 32);
+        }
+        if (!ok) return cudaErrorInvalidValue;
     }
-    if (!ok) return cudaErrorInvalidValue;
+    const DecayPass &p = set.p[0];
     const int bytes = sum ? (int)SumLayout<D1, D2>::BYTES : (int)PassLayout<D1, D2>::BYTES;
     const int threads = sum ? SumLayout<D1, D2>::THREADS : PassLayout<D1, D2>::THREADS;
     auto kern = sum ? decay_sum_tc_kernel<D1, D2> : decay_pass_tc_kernel<D1, D2>;
@@ -691,20 +732,16 @@ cudaError_t launch_one(const DecayPass &p, bool sum, cudaStream_t s) {
         if (!sum && attr.numRegs * threads < PassLayout<D1, D2>::SHARES) return cudaErrorInvalidKernelImage;
         if (dev < 64) ready[sum][dev] = true;
     }
-    launch_probe_mark(s);
-    kern<<<dim3(p.nseg, p.H, p.B), threads, bytes, s>>>(p, maps);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_widths(const DecayPass &p, bool sum, cudaStream_t s) {
-    if (p.d1 <= 64) return p.d2 <= 64 ? launch_one<64, 64>(p, sum, s) : launch_one<64, 128>(p, sum, s);
-    return p.d2 <= 64 ? launch_one<128, 64>(p, sum, s) : launch_one<128, 128>(p, sum, s);
+    return decay_launch(kern, dim3(set.count * p.nseg, p.H, p.B), threads, bytes, s, set.dependent, set, maps);
 }
 
 }  // namespace
 
-cudaError_t launch_decay_sum_tc(const DecayPass &p, cudaStream_t s) { return launch_widths(p, true, s); }
-cudaError_t launch_decay_pass_tc(const DecayPass &p, cudaStream_t s) { return launch_widths(p, false, s); }
+cudaError_t launch_decay_tc(const DecayPassSet &set, bool sum, cudaStream_t s) {
+    const int d1 = decay_padded(set.p[0].d1), d2 = decay_padded(set.p[0].d2);
+    if (d1 == 64) return d2 == 64 ? launch_one<64, 64>(set, sum, s) : launch_one<64, 128>(set, sum, s);
+    return d2 == 64 ? launch_one<128, 64>(set, sum, s) : launch_one<128, 128>(set, sum, s);
+}
 
 // Read and clear these kernels' status word (PRISM_OK or PRISM_ERR_TIMEOUT).
 cudaError_t decay_status(uint32_t *out) {
