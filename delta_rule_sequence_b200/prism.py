@@ -174,14 +174,15 @@ def _check_tensor(name, x, dtype, shape, device):
         return
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor (libprism has no CPU path)")
+    if x.dtype is dtype and x.shape == shape and x.device == device and x.is_contiguous():
+        return
     if x.device != device:
         raise ValueError(f"{name} is on {x.device}, q is on {device}")
     if x.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
     if x.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(x.shape)}")
-    if not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def make_shape(q, v=None, u=None, chunk=64, L=None) -> PrismShape:
@@ -518,16 +519,14 @@ def _launched_on(stream, device, *tensors) -> None:
 def _view_strides(name, x, dtype, shape, device):
     """Checks a tensor whose last dimension is dense and whose other strides are the library's to follow;
     returns those strides."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor (libprism has no CPU path)")
+    if x.dtype is dtype and x.shape == shape and x.device == device and x.is_contiguous():
+        return _DENSE
     if x.device != device:
         raise ValueError(f"{name} is on {x.device}, q is on {device}")
     if x.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
     if x.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(x.shape)}")
-    if x.is_contiguous():
-        return _DENSE
     strides = x.stride()
     if strides[-1] != 1:
         raise ValueError(f"{name} must have unit stride along its last dimension")
@@ -541,6 +540,16 @@ def _view_strides(name, x, dtype, shape, device):
 _DENSE = (0, 0, 0)  # prism_decay_shape: the dense layout
 
 
+@functools.lru_cache(maxsize=4096)
+def _decay_shape(sizes, *strides):
+    return PrismDecayShape(*sizes, *strides)  # read only by the library
+
+
+@functools.lru_cache(maxsize=4096)
+def _norm_shape(sizes):
+    return PrismNormShape(*sizes)
+
+
 def _decay_inputs(q, k, v, decay):
     """Checks shared by the decay scan's entry points; returns (shape, its sizes, device, io dtype)."""
     for name, x in (("q", q), ("k", k), ("v", v)):
@@ -549,19 +558,20 @@ def _decay_inputs(q, k, v, decay):
         if x.dim() != 4:
             raise ValueError(f"{name} must have 4 dimensions [B, T, heads, width], got {tuple(x.shape)}")
     dev, io = q.device, q.dtype
-    if io not in (torch.bfloat16, torch.float32):
+    if io is not torch.bfloat16 and io is not torch.float32:
         raise TypeError(f"q must be torch.bfloat16 or torch.float32, got {io}")
     B, T, H, dk = q.shape
     Hkv, dv = k.shape[2], v.shape[3]
     if Hkv < 1 or H % Hkv:
         raise ValueError(f"k has {Hkv} heads, which do not divide the {H} heads of q")
-    strides = (_view_strides("q", q, io, (B, T, H, dk), dev), _view_strides("k", k, io, (B, T, Hkv, dk), dev),
-               _view_strides("v", v, io, (B, T, Hkv, dv), dev))
+    qs = _view_strides("q", q, io, (B, T, H, dk), dev)
+    ks = _view_strides("k", k, io, (B, T, Hkv, dk), dev)
+    vs = _view_strides("v", v, io, (B, T, Hkv, dv), dev)
     if decay is None:
         raise TypeError("decay must be a CUDA tensor (libprism has no CPU path)")
     _check_tensor("decay", decay, torch.float32, (H,), dev)
-    sizes = (B, H, T, Hkv, dk, dv, PRISM_F32 if io == torch.float32 else PRISM_BF16)
-    return PrismDecayShape(*sizes, *strides), sizes, dev, io
+    sizes = (B, H, T, Hkv, dk, dv, PRISM_F32 if io is torch.float32 else PRISM_BF16)
+    return _decay_shape(sizes, qs, ks, vs), sizes, dev, io
 
 
 def prism_decay_scan_fwd(q, k, v, decay, S0=None, lengths=None, *, o=None, S_final=None, want_state=True,
@@ -665,7 +675,7 @@ def _norm_inputs(x, groups, weight, bias, gate, eps, activation):
     _check_tensor("bias", bias, torch.float32, (C,), dev)
     _check_tensor("gate", gate, io, x.shape, dev)
     sizes = (N, S, C, groups, PRISM_F32 if io == torch.float32 else PRISM_BF16, ACTIVATIONS[activation], float(eps))
-    return PrismNormShape(*sizes), sizes, dev, io
+    return _norm_shape(sizes), sizes, dev, io
 
 
 def prism_group_norm_fwd(x, groups, weight=None, bias=None, gate=None, *, eps=1e-5, activation="none", y=None,
