@@ -3,6 +3,7 @@
 // segments and the sum of shared heads' gradients for both types.
 
 #include "decay.cuh"
+#include "f32x2.cuh"
 
 namespace prism {
 namespace {
@@ -10,42 +11,96 @@ namespace {
 constexpr int CH = kDecayChunkSimt;  // tokens of a chunk
 constexpr int NT = 256;              // 16 x 16 threads
 
-// Tile rows [t0, t0 + CH) of one head into shared memory as fp32, zero beyond `len` tokens and beyond
-// the operand's own width d (tiles are D = 64 or 128 columns wide, rows D + 4 floats apart: 16-byte
+// Tile rows [t0, t0 + CH) of one head into shared memory by asynchronous copies, zero beyond `len` tokens and
+// beyond the operand's own width d (tiles are D = 64 or 128 columns wide, rows D + 4 floats apart: 16-byte
 // aligned, and 16 rows read at one column fall into different banks).
 template <int D>
-__device__ __forceinline__ void load_tile(float *dst, const DecayTensor &x, int b, int h, int t0, int len, int d) {
+__device__ __forceinline__ void request_tile(float *dst, const DecayTensor &x, int b, int h, int t0, int len, int d) {
     const float *src = (const float *)x.p + b * x.sb + (long long)(h / x.div) * x.sh;
     for (int e = threadIdx.x; e < CH * (D / 4); e += NT) {
         const int r = e / (D / 4), c = (e % (D / 4)) * 4;  // (d is a multiple of 32)
-        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (t0 + r < len && c < d) f = *reinterpret_cast<const float4 *>(src + (long long)(t0 + r) * x.st + c);
-        *reinterpret_cast<float4 *>(dst + r * (D + 4) + c) = f;
+        const bool in = t0 + r < len && c < d;
+        const float *from = in ? src + (long long)(t0 + r) * x.st + c : src;
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst + r * (D + 4) + c);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");
     }
+}
+__device__ __forceinline__ void request_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>  // all requests but the N latest have landed (this thread's)
+__device__ __forceinline__ void request_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Two rows of four floats as four packed pairs.
+__device__ __forceinline__ void lds4(const float *p, F2 (&v)[2]) {
+    const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(p);
+    v[0] = x.x;
+    v[1] = x.y;
 }
 
 // acc[r][c] += sum_j w_j Y[j][m0 + r] Z[j][n0 + c]: a thread's tile of the state, m along y, n along z
-// (4 consecutive columns out of every 64).
+// (4 consecutive columns out of every 64; pairs of columns packed).
 template <int D1, int D2>
-__device__ __forceinline__ void state_tile(const float *Y, const float *Z, const float *w, float (&acc)[D1 / 16][D2 / 16]) {
+__device__ __forceinline__ void state_tile(const float *Y, const float *Z, const float *w, F2 (&acc)[D1 / 16][D2 / 32]) {
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll 2
     for (int j = 0; j < CH; ++j) {
         const float wj = w[j];
-        float4 y[D1 / 64], z[D2 / 64];
+        F2 z[D2 / 64][2];
+#pragma unroll
+        for (int i = 0; i < D2 / 64; ++i) lds4(Z + j * (D2 + 4) + 64 * i + 4 * tx, z[i]);
 #pragma unroll
         for (int i = 0; i < D1 / 64; ++i) {
-            y[i] = *reinterpret_cast<const float4 *>(Y + j * (D1 + 4) + 64 * i + 4 * ty);
-            y[i].x *= wj; y[i].y *= wj; y[i].z *= wj; y[i].w *= wj;
+            const float4 y = *reinterpret_cast<const float4 *>(Y + j * (D1 + 4) + 64 * i + 4 * ty);
+            const float yf[4] = {y.x * wj, y.y * wj, y.z * wj, y.w * wj};
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const F2 yy = pack2(yf[r], yf[r]);
+#pragma unroll
+                for (int c = 0; c < D2 / 32; ++c) acc[4 * i + r][c] = fma(yy, z[c >> 1][c & 1], acc[4 * i + r][c]);
+            }
         }
-#pragma unroll
-        for (int i = 0; i < D2 / 64; ++i) z[i] = *reinterpret_cast<const float4 *>(Z + j * (D2 + 4) + 64 * i + 4 * tx);
-        const float *yf = &y[0].x, *zf = &z[0].x;
-#pragma unroll
-        for (int r = 0; r < D1 / 16; ++r)
-#pragma unroll
-            for (int c = 0; c < D2 / 16; ++c) acc[r][c] = fmaf(yf[r], zf[c], acc[r][c]);
     }
 }
+
+// o[r][c] += sum_k A[row r][k] B[k][n0 + c], rows ty + 16 r of A (pitch pa), K a multiple of 4.
+template <int D2>
+__device__ __forceinline__ void rows_tile(const float *A, int pa, const float *B, int K, F2 (&o)[4][D2 / 32]) {
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll 2
+    for (int k0 = 0; k0 < K; k0 += 4) {
+        float4 a[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) a[r] = *reinterpret_cast<const float4 *>(A + (ty + 16 * r) * pa + k0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            F2 b[D2 / 64][2];
+#pragma unroll
+            for (int i = 0; i < D2 / 64; ++i) lds4(B + (k0 + k) * (D2 + 4) + 64 * i + 4 * tx, b[i]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float x = (&a[r].x)[k];
+                const F2 xx = pack2(x, x);
+#pragma unroll
+                for (int c = 0; c < D2 / 32; ++c) o[r][c] = fma(xx, b[c >> 1][c & 1], o[r][c]);
+            }
+        }
+    }
+}
+
+// Floats of the chunk buffers (one set of tiles each) and of what follows them.  The next chunk's tiles are
+// requested before the current one's products, where two sets fit (all widths but 128 x 128 of the pass).
+template <int D1, int D2>
+struct SumSizes {
+    static constexpr int SET = CH * (D1 + 4) + CH * (D2 + 4), NB = 2;
+    static constexpr int TOTAL = NB * SET + (CH + 1) + CH;
+};
+template <int D1, int D2>
+struct PassSizes {
+    static constexpr int SET = 2 * CH * (D1 + 4) + CH * (D2 + 4);
+    static constexpr int REST = D1 * (D2 + 4) + CH * (CH + 4) + (CH + 1) + CH;
+    static constexpr int NB = 4 * (2 * SET + REST) <= 227 * 1024 ? 2 : 1;
+    static constexpr int TOTAL = NB * SET + REST;
+    static_assert(4 * TOTAL <= 227 * 1024, "shared memory budget");
+};
 
 // Column of the register tile's index i along y or z.
 __device__ __forceinline__ int tile_col(int i, int t) { return 64 * (i >> 2) + 4 * t + (i & 3); }
@@ -57,7 +112,8 @@ __device__ __forceinline__ int write_exponent(int j, int n, int reverse) { retur
 template <int D1, int D2>
 __global__ void __launch_bounds__(NT) decay_sum_simt_kernel(const __grid_constant__ DecayPassSet set) {
     extern __shared__ __align__(16) float sm[];
-    float *Y = sm, *Z = Y + CH * (D1 + 4), *pw = Z + CH * (D2 + 4), *w = pw + CH + 1;
+    using SZ = SumSizes<D1, D2>;
+    float *pw = sm + SZ::NB * SZ::SET, *w = pw + CH + 1;
     decay_wait();
     const DecayPass &p = set.p[blockIdx.x / set.p[0].nseg];
     const int seg = blockIdx.x % p.nseg, h = blockIdx.y, b = blockIdx.z;
@@ -66,20 +122,32 @@ __global__ void __launch_bounds__(NT) decay_sum_simt_kernel(const __grid_constan
     const int s1 = min(s0 + p.seg_tokens, len);
     const float a = p.decay[h];
     for (int i = threadIdx.x; i <= CH; i += NT) pw[i] = decay_pow(a, i);
-    float acc[D1 / 16][D2 / 16] = {};
+    F2 acc[D1 / 16][D2 / 32] = {};
     const int nch = s1 > s0 ? (s1 - s0 + CH - 1) / CH : 0;
+    auto token = [&](int cc) { return s0 + (p.reverse ? nch - 1 - cc : cc) * CH; };
+    auto request = [&](int cc) {
+        float *Y = sm + (cc % SZ::NB) * SZ::SET;
+        request_tile<D1>(Y, p.y, b, h, token(cc), len, p.d1);
+        request_tile<D2>(Y + CH * (D1 + 4), p.z, b, h, token(cc), len, p.d2);
+        request_commit();
+    };
+    if (nch > 0) request(0);
     for (int cc = 0; cc < nch; ++cc) {
-        const int t0 = s0 + (p.reverse ? nch - 1 - cc : cc) * CH;
-        const int n = min(CH, s1 - t0);
-        __syncthreads();
-        load_tile<D1>(Y, p.y, b, h, t0, len, p.d1);
-        load_tile<D2>(Z, p.z, b, h, t0, len, p.d2);
+        const int n = min(CH, s1 - token(cc));
+        const float *Y = sm + (cc % SZ::NB) * SZ::SET, *Z = Y + CH * (D1 + 4);
+        __syncthreads();  // the chunk before is done with
+        if (cc + 1 < nch) {
+            request(cc + 1);
+            request_wait<1>();
+        } else {
+            request_wait<0>();
+        }
         for (int j = threadIdx.x; j < CH; j += NT) w[j] = j < n ? pw[write_exponent(j, n, p.reverse)] : 0.f;
-        const float an = pw[n];
+        const F2 an = pack2(pw[n], pw[n]);
 #pragma unroll
         for (int r = 0; r < D1 / 16; ++r)
 #pragma unroll
-            for (int c = 0; c < D2 / 16; ++c) acc[r][c] *= an;
+            for (int c = 0; c < D2 / 32; ++c) acc[r][c] = mul(acc[r][c], an);
         __syncthreads();
         state_tile<D1, D2>(Y, Z, w, acc);
     }
@@ -91,7 +159,7 @@ __global__ void __launch_bounds__(NT) decay_sum_simt_kernel(const __grid_constan
 #pragma unroll
         for (int c = 0; c < D2 / 16; ++c) {
             const int n = tile_col(c, tx);
-            if (m < p.d1 && n < p.d2) F[n * p.d1 + m] = acc[r][c];
+            if (m < p.d1 && n < p.d2) F[n * p.d1 + m] = c & 1 ? second(acc[r][c >> 1]) : first(acc[r][c >> 1]);
         }
     }
 }
@@ -102,8 +170,8 @@ template <int D1, int D2>
 __global__ void __launch_bounds__(NT) decay_pass_simt_kernel(const __grid_constant__ DecayPassSet set) {
     extern __shared__ __align__(16) float sm[];
     constexpr int PP = CH + 4;
-    float *X = sm, *Y = X + CH * (D1 + 4), *Z = Y + CH * (D1 + 4), *R = Z + CH * (D2 + 4), *P = R + D1 * (D2 + 4),
-          *pw = P + CH * PP, *w = pw + CH + 1;
+    using SZ = PassSizes<D1, D2>;
+    float *R = sm + SZ::NB * SZ::SET, *P = R + D1 * (D2 + 4), *pw = P + CH * PP, *w = pw + CH + 1;
     decay_wait();
     const DecayPass &p = set.p[blockIdx.x / set.p[0].nseg];
     const int seg = blockIdx.x % p.nseg, h = blockIdx.y, b = blockIdx.z;
@@ -121,126 +189,100 @@ __global__ void __launch_bounds__(NT) decay_pass_simt_kernel(const __grid_consta
         if (E && m < p.d1 && n < p.d2) x = E[p.entry_t ? m * p.d2 + n : n * p.d1 + m];
         R[m * (D2 + 4) + n] = x;
     }
-    auto store = [&](int t, int n, float x) {
-        const long long at = (((long long)b * p.T + t) * p.H + h) * p.d2 + n;
-        ((float *)p.o)[at] = x;
-    };
     const int nch = s1 > s0 ? (s1 - s0 + CH - 1) / CH : 0;
+    auto token = [&](int cc) { return s0 + (p.reverse ? nch - 1 - cc : cc) * CH; };
+    auto request = [&](int cc) {
+        float *X = sm + (cc % SZ::NB) * SZ::SET;
+        request_tile<D1>(X, p.x, b, h, token(cc), len, p.d1);
+        request_tile<D1>(X + CH * (D1 + 4), p.y, b, h, token(cc), len, p.d1);
+        request_tile<D2>(X + 2 * CH * (D1 + 4), p.z, b, h, token(cc), len, p.d2);
+        request_commit();
+    };
+    if (SZ::NB == 2 && nch > 0) request(0);
     for (int cc = 0; cc < nch; ++cc) {
-        const int t0 = s0 + (p.reverse ? nch - 1 - cc : cc) * CH;
-        const int n = min(CH, s1 - t0);
-        __syncthreads();
-        load_tile<D1>(X, p.x, b, h, t0, len, p.d1);
-        load_tile<D1>(Y, p.y, b, h, t0, len, p.d1);
-        load_tile<D2>(Z, p.z, b, h, t0, len, p.d2);
+        const int t0 = token(cc), n = min(CH, s1 - t0);
+        const float *X = sm + (cc % SZ::NB) * SZ::SET, *Y = X + CH * (D1 + 4), *Z = Y + CH * (D1 + 4);
+        __syncthreads();  // the chunk before is done with
+        if (SZ::NB == 1) request(cc);
+        if (SZ::NB == 2 && cc + 1 < nch) {
+            request(cc + 1);
+            request_wait<1>();
+        } else {
+            request_wait<0>();
+        }
         for (int j = threadIdx.x; j < CH; j += NT) w[j] = j < n ? pw[write_exponent(j, n, p.reverse)] : 0.f;
         __syncthreads();
         // P[i][j] = a^|i-j| x_i . y_j on the causal side, rows i = ty + 16 r, columns j = tx + 16 c
         {
-            float s[4][4] = {};
+            F2 s2[4][4] = {};  // sums over even and odd columns
+#pragma unroll 2
             for (int d = 0; d < D1; d += 4) {
-                float4 xv[4], yv[4];
+                F2 xv[4][2], yv[4][2];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    xv[r] = *reinterpret_cast<const float4 *>(X + (ty + 16 * r) * (D1 + 4) + d);
-                    yv[r] = *reinterpret_cast<const float4 *>(Y + (tx + 16 * r) * (D1 + 4) + d);
+                    lds4(X + (ty + 16 * r) * (D1 + 4) + d, xv[r]);
+                    lds4(Y + (tx + 16 * r) * (D1 + 4) + d, yv[r]);
                 }
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        s[r][c] = fmaf(xv[r].x, yv[c].x, fmaf(xv[r].y, yv[c].y, fmaf(xv[r].z, yv[c].z, fmaf(xv[r].w, yv[c].w, s[r][c]))));
+                    for (int c = 0; c < 4; ++c) s2[r][c] = fma(xv[r][0], yv[c][0], fma(xv[r][1], yv[c][1], s2[r][c]));
             }
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int i = ty + 16 * r, j = tx + 16 * c, gap = p.reverse ? j - i : i - j;
-                    P[i * PP + j] = gap >= 0 ? s[r][c] * pw[gap] : 0.f;
+                    P[i * PP + j] = gap >= 0 ? total(s2[r][c]) * pw[gap] : 0.f;
                 }
         }
         __syncthreads();
-        float o[4][D2 / 16] = {};
+        F2 o[4][D2 / 32] = {};
         // entry term, then scaled by its row's decay, then the chunk's own
-        for (int d = 0; d < D1; d += 4) {
-            float4 xv[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) xv[r] = *reinterpret_cast<const float4 *>(X + (ty + 16 * r) * (D1 + 4) + d);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int c4 = 0; c4 < D2 / 64; ++c4) {
-                    const float4 z = *reinterpret_cast<const float4 *>(R + (d + k) * (D2 + 4) + 64 * c4 + 4 * tx);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float x = (&xv[r].x)[k];
-                        o[r][4 * c4] = fmaf(x, z.x, o[r][4 * c4]);
-                        o[r][4 * c4 + 1] = fmaf(x, z.y, o[r][4 * c4 + 1]);
-                        o[r][4 * c4 + 2] = fmaf(x, z.z, o[r][4 * c4 + 2]);
-                        o[r][4 * c4 + 3] = fmaf(x, z.w, o[r][4 * c4 + 3]);
-                    }
-                }
-        }
+        rows_tile<D2>(X, D1 + 4, R, D1, o);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int i = ty + 16 * r;
             const float f = i < n ? pw[p.reverse ? n - 1 - i : i + 1] : 0.f;
 #pragma unroll
-            for (int c = 0; c < D2 / 16; ++c) o[r][c] *= f;
+            for (int c = 0; c < D2 / 32; ++c) o[r][c] = mul(o[r][c], pack2(f, f));
         }
-        for (int j = 0; j < CH; j += 4) {
-            float4 xv[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) xv[r] = *reinterpret_cast<const float4 *>(P + (ty + 16 * r) * PP + j);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int c4 = 0; c4 < D2 / 64; ++c4) {
-                    const float4 z = *reinterpret_cast<const float4 *>(Z + (j + k) * (D2 + 4) + 64 * c4 + 4 * tx);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float x = (&xv[r].x)[k];
-                        o[r][4 * c4] = fmaf(x, z.x, o[r][4 * c4]);
-                        o[r][4 * c4 + 1] = fmaf(x, z.y, o[r][4 * c4 + 1]);
-                        o[r][4 * c4 + 2] = fmaf(x, z.z, o[r][4 * c4 + 2]);
-                        o[r][4 * c4 + 3] = fmaf(x, z.w, o[r][4 * c4 + 3]);
-                    }
-                }
-        }
+        rows_tile<D2>(P, PP, Z, CH, o);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int i = ty + 16 * r;
             if (i >= n) continue;
 #pragma unroll
-            for (int c = 0; c < D2 / 16; ++c) {
-                const int col = tile_col(c, tx);
-                if (col < p.d2) store(t0 + i, col, o[r][c]);
+            for (int c = 0; c < D2 / 64; ++c) {
+                const int col = 64 * c + 4 * tx;
+                if (col < p.d2)
+                    *reinterpret_cast<ulonglong2 *>((float *)p.o + (((long long)b * p.T + t0 + i) * p.H + h) * p.d2 + col) =
+                        make_ulonglong2(o[r][2 * c], o[r][2 * c + 1]);
             }
         }
         if (cc + 1 < nch) {
-            float acc[D1 / 16][D2 / 16] = {};
+            F2 acc[D1 / 16][D2 / 32] = {};
             state_tile<D1, D2>(Y, Z, w, acc);
             __syncthreads();  // every thread has read R for its outputs
-            const float an = pw[n];
+            const F2 an = pack2(pw[n], pw[n]);
 #pragma unroll
             for (int r = 0; r < D1 / 16; ++r)
 #pragma unroll
-                for (int c = 0; c < D2 / 16; ++c) {
-                    float &x = R[tile_col(r, ty) * (D2 + 4) + tile_col(c, tx)];
-                    x = fmaf(an, x, acc[r][c]);
+                for (int c = 0; c < D2 / 32; ++c) {
+                    F2 &x = *reinterpret_cast<F2 *>(R + tile_col(r, ty) * (D2 + 4) + tile_col(2 * c, tx));
+                    x = fma(an, x, acc[r][c]);
                 }
         }
     }
     // rows behind the sequence's last token
     const int z0 = max(s0, s1);
-    for (int e = threadIdx.x; e < (send - z0) * p.d2; e += NT) store(z0 + e / p.d2, e % p.d2, 0.f);
+    for (int e = threadIdx.x; e < (send - z0) * p.d2; e += NT) ((float *)p.o)[(((long long)b * p.T + z0 + e / p.d2) * p.H + h) * p.d2 + e % p.d2] = 0.f;
 }
 
 template <int D1, int D2>
 cudaError_t launch_one(const DecayPassSet &set, bool sum, cudaStream_t s) {
     const DecayPass &p = set.p[0];
-    const int tiles = CH * (D1 + 4) + CH * (D2 + 4) + CH + 1 + CH;
-    const int bytes = 4 * (sum ? tiles : tiles + CH * (D1 + 4) + D1 * (D2 + 4) + CH * (CH + 4));
+    const int bytes = 4 * (sum ? SumSizes<D1, D2>::TOTAL : PassSizes<D1, D2>::TOTAL);
     auto kern = sum ? decay_sum_simt_kernel<D1, D2> : decay_pass_simt_kernel<D1, D2>;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (err != cudaSuccess) return err;

@@ -20,6 +20,7 @@
 
 #include "api.cuh"
 #include "common.cuh"
+#include "f32x2.cuh"
 
 namespace prism {
 namespace {
@@ -84,44 +85,16 @@ __device__ __forceinline__ float act_both(int act, float z, float &slope) {
 //
 // A unit of one element is a float, of two a 64-bit register pair.
 
-using F2 = unsigned long long;
 template <int V>
 using Unit = std::conditional_t<V == 1, float, F2>;
 template <int V>
 constexpr int kUnits = V == 1 ? 1 : V / 2;
 
-__device__ __forceinline__ F2 pack2(float a, float b) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float first(F2 r) { return __uint_as_float((uint32_t)r); }
-__device__ __forceinline__ float second(F2 r) { return __uint_as_float((uint32_t)(r >> 32)); }
 template <typename U>
 __device__ __forceinline__ U both(float x) {
     if constexpr (sizeof(U) == 4) return x;
     else return pack2(x, x);
 }
-__device__ __forceinline__ float add(float a, float b) { return a + b; }
-__device__ __forceinline__ float mul(float a, float b) { return a * b; }
-__device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
-__device__ __forceinline__ F2 add(F2 a, F2 b) {
-    F2 d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ F2 mul(F2 a, F2 b) {
-    F2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
-    F2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ float total(float a) { return a; }
-__device__ __forceinline__ float total(F2 a) { return first(a) + second(a); }
 
 // ---- vectors of V consecutive channels -----------------------------------------------------------
 
