@@ -16,6 +16,7 @@
 // write nothing.
 
 #include "decay.cuh"
+#include "f32x2.cuh"
 #include "tc.cuh"
 #include "tensor_map.cuh"
 
@@ -128,6 +129,39 @@ __device__ __forceinline__ void weigh(const uint8_t *Y, int m, const float *w, i
     }
 }
 
+// The same for 64-wide Y (D1 = 64), whose product needs only M = 64 rows: the weighted tile goes to shared
+// memory in Y's own layout (an MN-major A operand), TERMS tiles one after the other, 16 bytes at a time by any
+// thread.  A TMEM operand's lanes are its rows, so half of the warps had none to write (2400 cycles a chunk).
+template <int TERMS>
+__device__ __forceinline__ void weigh_tile64(const uint8_t *Y, uint8_t *out, const float *w, int n, int tid, int nthreads) {
+    for (int e = tid; e < CT * 8; e += nthreads) {
+        const int row = e >> 3;
+        const uint4 raw = *reinterpret_cast<const uint4 *>(Y + e * 16);  // (a row's chunks may be read in any order)
+        const uint32_t y[4] = {raw.x, raw.y, raw.z, raw.w};
+        const F2 ww = pack2(w[row], w[row]);
+        F2 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = row < n ? mul(pack2(lo_f(y[i]), hi_f(y[i])), ww) : 0ull;
+#pragma unroll
+        for (int k = 0; k < TERMS; ++k) {
+            uint32_t t[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                t[i] = bf16_pair(first(x[i]), second(x[i]));
+                if (k + 1 < TERMS) x[i] = add(x[i], pack2(-lo_f(t[i]), -hi_f(t[i])));
+            }
+            *reinterpret_cast<uint4 *>(out + k * kBlk + e * 16) = make_uint4(t[0], t[1], t[2], t[3]);
+        }
+    }
+}
+
+// Where row m = 16 (lane quarter) + lane of an M = 64 product sits: the first 16 lanes of each quarter.  M = 128:
+// row = lane.
+template <int D1>
+__device__ __forceinline__ int product_row(int q, int lane) { return D1 == 64 ? 16 * q + lane : 32 * q + lane; }
+template <int D1>
+__device__ __forceinline__ bool product_lane(int lane) { return D1 != 64 || lane < 16; }
+
 // Zero rows n .. 127 of a tile (by `nthreads` threads), so that what lies behind the sequence's end
 // reaches no product.
 template <int D>
@@ -147,11 +181,14 @@ struct SumLayout {
     static constexpr int YW = 8, SW = 8;                 // warps that weigh Y, that hold the state
     static constexpr int LOADW = YW + SW, MMAW = LOADW + 1;
     static constexpr int THREADS = 32 * (MMAW + 1);
-    static constexpr int NST = 227 * 1024 / (tile_bytes<D1>() + tile_bytes<D2>() + 1024) > 4 ? 4 : 3;
+    // The weighted Y: two buffers of three terms in TMEM, or (D1 = 64) one or two in shared memory.
+    static constexpr int NYB = D1 == 64 && D2 == 128 ? 1 : 2;
+    static constexpr int NST = 3;
     static constexpr uint32_t STAGE = tile_bytes<D1>() + tile_bytes<D2>();
-    static constexpr uint32_t BYTES = NST * STAGE + 1024;
-    static constexpr uint32_t cY = 0, cD = 384;          // TMEM: two buffers of three terms, the product
-    static_assert(BYTES <= 227 * 1024, "shared memory budget");
+    static constexpr uint32_t YP = NST * STAGE, YP_BYTES = D1 == 64 ? 3 * kBlk : 0;
+    static constexpr uint32_t BYTES = YP + NYB * YP_BYTES + 1024;
+    static constexpr uint32_t cY = 0, cD = 384;          // TMEM columns: the weighted Y, the product
+    static_assert(BYTES + 2048 <= 227 * 1024, "shared memory budget");
 };
 
 template <int D1, int D2>
@@ -163,7 +200,7 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
     constexpr int NST = LY::NST;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    __shared__ uint64_t full[NST], freeb[NST], yp_full[2], yp_free[2], d_full, d_free, drain;
+    __shared__ uint64_t full[NST], freeb[NST], yp_full[LY::NYB], yp_free[LY::NYB], d_full, d_free, drain;
     __shared__ Powers pw;
     __shared__ __align__(16) float w_last[CT];  // the weights of the walk's last chunk
     __shared__ uint32_t tmem_base_sh;
@@ -180,7 +217,7 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
             mbar_init(&full[i], 1);
             mbar_init(&freeb[i], LY::YW + 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < LY::NYB; ++i) {
             mbar_init(&yp_full[i], LY::YW);
             mbar_init(&yp_free[i], 1);
         }
@@ -216,22 +253,29 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
         }
     } else if (warp == LY::MMAW) {
         {
-            const uint32_t id = idesc_bf16(128, D2, 0, 1);
+            const uint32_t id = D1 == 64 ? idesc_bf16(64, D2, 1, 1) : idesc_bf16(128, D2, 0, 1);
             auto oz = [](int ks) { return (uint64_t)koff_mn_sw128(ks); };
             auto oy = [](int ks) { return 8 * ks; };
             for (int i = 0; i < wk.nch; ++i) {
-                const int st = i % NST, pb = i & 1;
+                const int st = i % NST, pb = i % LY::NYB;
                 if (!mbar_wait_suspend(&full[st], (uint32_t)((i / NST) & 1), status, lim) ||
-                    !mbar_wait_suspend(&yp_full[pb], (uint32_t)((i >> 1) & 1), status, lim) ||
+                    !mbar_wait_suspend(&yp_full[pb], (uint32_t)((i / LY::NYB) & 1), status, lim) ||
                     (i > 0 && !mbar_wait_suspend(&d_free, (uint32_t)((i - 1) & 1), status, lim)))
                     break;
                 fence_after_sync();
                 const uint64_t dz = make_desc(smem_u32(sm + st * LY::STAGE + tile_bytes<D1>()), kBlk, 1024, 2);
-                const uint32_t ya = tb + LY::cY + pb * 192;
                 // smallest terms first: their sum loses nothing to the large one's magnitude
-                mma_steps_tmem_a_warp<CT / 16>(tb + LY::cD, id, ya + 128, dz, oy, oz, false);
-                mma_steps_tmem_a_warp<CT / 16>(tb + LY::cD, id, ya + 64, dz, oy, oz, true);
-                mma_steps_tmem_a_warp<CT / 16>(tb + LY::cD, id, ya, dz, oy, oz, true);
+                if constexpr (D1 == 64) {
+                    const uint32_t yp = smem_u32(sm + LY::YP + pb * LY::YP_BYTES);
+#pragma unroll
+                    for (int k = 2; k >= 0; --k)
+                        mma_steps_warp<CT / 16>(tb + LY::cD, id, make_desc(yp + k * kBlk, kBlk, 1024, 2), dz, oz, oz, k < 2);
+                } else {
+                    const uint32_t ya = tb + LY::cY + pb * 192;
+#pragma unroll
+                    for (int k = 2; k >= 0; --k)
+                        mma_steps_tmem_a_warp<CT / 16>(tb + LY::cD, id, ya + 64 * k, dz, oy, oz, k < 2);
+                }
                 mma_commit_warp(&d_full);
                 mma_commit_warp(&yp_free[pb]);
                 mma_commit_warp(&freeb[st]);
@@ -242,23 +286,23 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
     } else if (warp < LY::YW) {
         const int q = warp & 3, half = warp >> 2, m = 32 * q + lane;
         for (int i = 0; i < wk.nch; ++i) {
-            const int st = i % NST, pb = i & 1, n = wk.n(i);
+            const int st = i % NST, pb = i % LY::NYB, n = wk.n(i);
             uint8_t *s = sm + st * LY::STAGE;
             if (!mbar_wait_suspend(&full[st], (uint32_t)((i / NST) & 1), status, lim) ||
-                (i >= 2 && !mbar_wait_suspend(&yp_free[pb], (uint32_t)(((i >> 1) - 1) & 1), status, lim)))
+                (i >= LY::NYB && !mbar_wait_suspend(&yp_free[pb], (uint32_t)((i / LY::NYB - 1) & 1), status, lim)))
                 break;
             fence_after_sync();
-            if (n < CT) {
-                zero_rows<D2>(s + tile_bytes<D1>(), n, tid, 32 * LY::YW);
-                fence_async_smem();
-            }
-            if (32 * q < D1) {
-                const float *w = i + 1 < wk.nch ? pw.w : w_last;
+            const float *w = i + 1 < wk.nch ? pw.w : w_last;
+            if (n < CT) zero_rows<D2>(s + tile_bytes<D1>(), n, tid, 32 * LY::YW);
+            if constexpr (D1 == 64) {
+                weigh_tile64<3>(s, sm + LY::YP + pb * LY::YP_BYTES, w, n, tid, 32 * LY::YW);
+            } else {
 #pragma unroll 1
                 for (int j0 = 64 * half; j0 < 64 * half + 64; j0 += kWeigh)
                     weigh<3>(s, m, w, j0, n, taddr(tb, 32 * q, 0), LY::cY + pb * 192);
                 tmem_wait_st();
             }
+            if (D1 == 64 || n < CT) fence_async_smem();
             fence_before_sync();
             __syncwarp();
             if (lane == 0) {
@@ -267,7 +311,7 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
             }
         }
     } else {
-        const int sw = warp - LY::YW, q = sw & 3, half = sw >> 2, m = 32 * q + lane;
+        const int sw = warp - LY::YW, q = sw & 3, half = sw >> 2, m = product_row<D1>(q, lane);
         constexpr int NC = D2 / 2;
         float r[NC];
 #pragma unroll
@@ -277,21 +321,19 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
             const float an = pw.at(wk.n(i));
             if (!mbar_wait_suspend(&d_full, (uint32_t)(i & 1), status, lim)) { ok = false; break; }
             fence_after_sync();
-            if (32 * q < D1) {
 #pragma unroll
-                for (int c = 0; c < NC; c += 32) {
-                    float d[32];
-                    tmem_ld32(taddr(tb, 32 * q, LY::cD + half * NC + c), d);
-                    tmem_wait_ld();
+            for (int c = 0; c < NC; c += 32) {
+                float d[32];
+                tmem_ld32(taddr(tb, 32 * q, LY::cD + half * NC + c), d);
+                tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) r[c + k] = fmaf(an, r[c + k], d[k]);
-                }
+                for (int k = 0; k < 32; ++k) r[c + k] = fmaf(an, r[c + k], d[k]);
             }
             fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&d_free);
         }
-        if (ok && m < p.d1) {
+        if (ok && product_lane<D1>(lane) && m < p.d1) {
             float *F = p.F + (((long long)wk.b * p.H + wk.h) * p.nseg + wk.seg) * p.d1 * p.d2 + m;
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
@@ -320,15 +362,19 @@ struct PassLayout {
     static constexpr int RS = 96, RP = 56, RO = 56, RY = 56, RM = 40;
     static constexpr int SHARES = (SW * RS + PW * RP + OW * RO + YW * RY + 4 * RM) * 32;
     static_assert(THREADS == 1024 && SHARES <= 64 * THREADS, "register shares");
-    static constexpr int NST = D1 == 64 ? (D2 == 64 ? 4 : 3) : 2;
+    static constexpr int NST = D1 == 64 && D2 == 64 ? 3 : 2;
     static constexpr uint32_t X = 0, Y = tile_bytes<D1>(), Z = 2 * tile_bytes<D1>();
     static constexpr uint32_t STAGE = 2 * tile_bytes<D1>() + tile_bytes<D2>();
     static constexpr uint32_t R = NST * STAGE;            // R^T as bf16: rows along y, columns along z
     static constexpr uint32_t R_BLK = D1 * 128;
-    static constexpr uint32_t BYTES = R + R_BLK * (D2 / 64) + 1024;
-    static constexpr uint32_t cP = 0, cO = 128, cD = 128 + D2, cY = 128 + 2 * D2;  // TMEM columns
+    static constexpr uint32_t YP = R + R_BLK * (D2 / 64), YP_BYTES = D1 == 64 ? 2 * kBlk : 0;  // the weighted Y (or in TMEM)
+    static constexpr uint32_t BYTES = YP + YP_BYTES + 1024;
+    // TMEM columns: P twice where there is room, so that the next chunk's P is computed while this one's is weighted
+    // (not at 128 x 128: 2 x 128 for P, 128 each for the outputs, the write and the weighted Y)
+    static constexpr int NPB = D1 == 128 && D2 == 128 ? 1 : 2;
+    static constexpr uint32_t cP = 0, cO = NPB * 128, cD = cO + D2, cY = cD + D2;
     static_assert(BYTES + 1024 <= 227 * 1024, "shared memory budget");
-    static_assert(cY + 128 <= 512, "TMEM columns");
+    static_assert(cY + (D1 == 64 ? 0 : 128) <= 512, "TMEM columns");
 };
 
 template <int D1, int D2>
@@ -341,7 +387,7 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     __shared__ uint64_t x_full[NST], y_full[NST], z_full[NST], x_free[NST], y_free[NST], z_free[NST];
-    __shared__ uint64_t p_full, p_ready, qs_full, o_scaled, o_full, o_free, s_ready, ds_full, yp_full, yp_free, drain;
+    __shared__ uint64_t p_full[LY::NPB], p_ready[LY::NPB], qs_full, o_scaled, o_full, o_free, s_ready, ds_full, yp_full, yp_free, drain;
     __shared__ Powers pw;
     __shared__ uint32_t tmem_base_sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -360,8 +406,10 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
             mbar_init(&y_free[i], LY::YW + 1);
             mbar_init(&z_free[i], LY::OW);
         }
-        mbar_init(&p_full, 1);
-        mbar_init(&p_ready, LY::PW);
+        for (int i = 0; i < LY::NPB; ++i) {
+            mbar_init(&p_full[i], 1);
+            mbar_init(&p_ready[i], LY::PW);
+        }
         mbar_init(&qs_full, 1);
         mbar_init(&o_scaled, LY::OW);
         mbar_init(&o_full, 1);
@@ -406,24 +454,31 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
         }
     } else if (warp == LY::MMAW) {
         {
-            const uint32_t idP = idesc_bf16(128, 128, 0, 0), idZ = idesc_bf16(128, D2, 0, 1);
+            const uint32_t idP = idesc_bf16(128, 128, 0, 0), idZ = idesc_bf16(128, D2, 0, 1), idY = idesc_bf16(64, D2, 1, 1);
             auto ok_ = [](int ks) { return (uint64_t)koff_k_sw128(ks, kBlk); };
             auto omn = [](int ks) { return (uint64_t)koff_mn_sw128(ks); };
             auto oy = [](int ks) { return 8 * ks; };
             auto op = [](int ks) { return 8 * ks + (ks >= 4 ? 32 : 0); };  // P': 64 tokens in each half of P
             const uint64_t dR = make_desc(smem_u32(sm + LY::R), LY::R_BLK, 1024, 2);
-            for (int i = 0; i < wk.nch; ++i) {
+            // P of chunk i (its region's last readers are products issued before)
+            auto issue_P = [&](int i) {
                 const int st = i % NST;
+                const uint32_t par = (uint32_t)((i / NST) & 1), s = smem_u32(sm + st * LY::STAGE);
+                if (!mbar_wait_suspend(&x_full[st], par, status, lim) || !mbar_wait_suspend(&y_full[st], par, status, lim)) return false;
+                fence_after_sync();
+                mma_steps_warp<D1 / 16>(tb + LY::cP + 128 * (i % LY::NPB), idP, make_desc(s + LY::X, 16, 1024, 2),
+                                        make_desc(s + LY::Y, 16, 1024, 2), ok_, ok_, false);
+                mma_commit_warp(&p_full[i % LY::NPB]);
+                mma_commit_warp(&y_free[st]);
+                return true;
+            };
+            bool go = LY::NPB == 1 || wk.nch == 0 || issue_P(0);
+            for (int i = 0; i < wk.nch && go; ++i) {
+                const int st = i % NST, pb = i % LY::NPB;
                 const uint32_t par = (uint32_t)((i / NST) & 1), ph = (uint32_t)(i & 1), before = (uint32_t)((i - 1) & 1);
                 const uint32_t s = smem_u32(sm + st * LY::STAGE);
-                const uint64_t dX = make_desc(s + LY::X, 16, 1024, 2), dY = make_desc(s + LY::Y, 16, 1024, 2),
-                               dZ = make_desc(s + LY::Z, kBlk, 1024, 2);
-                if (!mbar_wait_suspend(&x_full[st], par, status, lim) || !mbar_wait_suspend(&y_full[st], par, status, lim)) break;
-                fence_after_sync();
-                // P (its region's last readers were the previous chunk's P' Z products, issued before)
-                mma_steps_warp<D1 / 16>(tb + LY::cP, idP, dX, dY, ok_, ok_, false);
-                mma_commit_warp(&p_full);
-                mma_commit_warp(&y_free[st]);
+                const uint64_t dX = make_desc(s + LY::X, 16, 1024, 2), dZ = make_desc(s + LY::Z, kBlk, 1024, 2);
+                if (LY::NPB == 1 ? !issue_P(i) : i + 1 < wk.nch && !issue_P(i + 1)) break;
                 // X R^T
                 if (!mbar_wait_suspend(&s_ready, ph, status, lim) || (i > 0 && !mbar_wait_suspend(&o_free, before, status, lim))) break;
                 fence_after_sync();
@@ -434,15 +489,21 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
                 if (!mbar_wait_suspend(&yp_full, ph, status, lim) || !mbar_wait_suspend(&z_full[st], par, status, lim)) break;
                 fence_after_sync();
                 if (i + 1 < wk.nch) {
-                    mma_steps_tmem_a_warp<CT / 16>(tb + LY::cD, idZ, tb + LY::cY + 64, dZ, oy, omn, false);
-                    mma_steps_tmem_a_warp<CT / 16>(tb + LY::cD, idZ, tb + LY::cY, dZ, oy, omn, true);
+                    if constexpr (D1 == 64) {
+                        const uint32_t yp = smem_u32(sm + LY::YP);
+                        mma_steps_warp<CT / 16>(tb + LY::cD, idY, make_desc(yp + kBlk, kBlk, 1024, 2), dZ, omn, omn, false);
+                        mma_steps_warp<CT / 16>(tb + LY::cD, idY, make_desc(yp, kBlk, 1024, 2), dZ, omn, omn, true);
+                    } else {
+                        mma_steps_tmem_a_warp<CT / 16>(tb + LY::cD, idZ, tb + LY::cY + 64, dZ, oy, omn, false);
+                        mma_steps_tmem_a_warp<CT / 16>(tb + LY::cD, idZ, tb + LY::cY, dZ, oy, omn, true);
+                    }
                     mma_commit_warp(&ds_full);
                     mma_commit_warp(&yp_free);
                 }
                 // O += P' Z
-                if (!mbar_wait_suspend(&p_ready, ph, status, lim) || !mbar_wait_suspend(&o_scaled, ph, status, lim)) break;
+                if (!mbar_wait_suspend(&p_ready[pb], (uint32_t)((i / LY::NPB) & 1), status, lim) || !mbar_wait_suspend(&o_scaled, ph, status, lim)) break;
                 fence_after_sync();
-                mma_steps_tmem_a_warp<CT / 16>(tb + LY::cO, idZ, tb + LY::cP, dZ, op, omn, true);
+                mma_steps_tmem_a_warp<CT / 16>(tb + LY::cO, idZ, tb + LY::cP + 128 * pb, dZ, op, omn, true);
                 mma_commit_warp(&o_full);
             }
             mma_commit_warp(&drain);
@@ -455,10 +516,10 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
         // ---------------- P' = a^|i-j| P on the causal side, as bf16 over P ----------------
         // two warps per 32 rows, 64 columns each, whose bf16 values go to the first 32 of the warp's own
         const int q = warp & 3, half = warp >> 2, row = 32 * q + lane;
-        const uint32_t tl = taddr(tb, 32 * q, LY::cP);
         for (int i = 0; i < wk.nch; ++i) {
-            const int n = wk.n(i);
-            if (!mbar_wait_suspend(&p_full, (uint32_t)(i & 1), status, lim)) break;
+            const int n = wk.n(i), pb = i % LY::NPB;
+            const uint32_t tl = taddr(tb, 32 * q, LY::cP + 128 * pb);
+            if (!mbar_wait_suspend(&p_full[pb], (uint32_t)((i / LY::NPB) & 1), status, lim)) break;
             fence_after_sync();
             // 16 columns at a time, in a loop: unrolled, the five roles' code of a chunk no longer fits the
             // instruction cache and every role waits for its instructions (P' took 7000 cycles instead of 1400)
@@ -508,7 +569,7 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
             tmem_wait_st();
             fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_ready);
+            if (lane == 0) mbar_arrive(&p_ready[pb]);
         }
     } else if (warp < LY::SW0) {
         setmaxnreg_dec<LY::RO>();
@@ -522,14 +583,14 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
             if (!mbar_wait_suspend(&qs_full, (uint32_t)(i & 1), status, lim)) break;
             fence_after_sync();
 #pragma unroll 1
-            for (int c = 0; c < D2; c += 16) {
-                float v[16];
-                tmem_ld16(tl + c, v);
+            for (int c = 0; c < D2; c += 32) {
+                float v[32];
+                tmem_ld32(tl + c, v);
                 tmem_wait_ld();
-                uint32_t u[16];
+                uint32_t u[32];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(v[k] * f);
-                tmem_st16(tl + c, u);
+                for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(v[k] * f);
+                tmem_st32(tl + c, u);
             }
             tmem_wait_st();
             fence_before_sync();
@@ -567,18 +628,18 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
                 }
             } else {
 #pragma unroll 1
-                for (int c = 0; c < D2; c += 16) {
-                    float v[16];
-                    tmem_ld16(tl + c, v);
+                for (int c = 0; c < D2; c += 32) {
+                    float v[32];
+                    tmem_ld32(tl + c, v);
                     tmem_wait_ld();
+                    if (!live)
 #pragma unroll
-                    for (int k = 0; k < 16; k += 8) {
-                        uint4 u = make_uint4(0, 0, 0, 0);
-                        if (live)
-                            u = make_uint4(bf16_pair(v[k], v[k + 1]), bf16_pair(v[k + 2], v[k + 3]),
-                                           bf16_pair(v[k + 4], v[k + 5]), bf16_pair(v[k + 6], v[k + 7]));
-                        *reinterpret_cast<uint4 *>(zs + sw128_off(row, c + k, kBlk)) = u;
-                    }
+                        for (int k = 0; k < 32; ++k) v[k] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8)
+                        *reinterpret_cast<uint4 *>(zs + sw128_off(row, c + k, kBlk)) =
+                            make_uint4(bf16_pair(v[k], v[k + 1]), bf16_pair(v[k + 2], v[k + 3]),
+                                       bf16_pair(v[k + 4], v[k + 5]), bf16_pair(v[k + 6], v[k + 7]));
                 }
                 fence_async_smem();
                 __syncwarp();
@@ -600,13 +661,14 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
         if (lane == 0) bulk_wait_all();
     } else if (warp < LY::YW0) {
         setmaxnreg_inc<LY::RS>();
-        // ---------------- the state: R^T[m][n] of row m = lane, half of the columns ----------------
-        const int sw = warp - LY::SW0, q = sw & 3, half = sw >> 2, m = 32 * q + lane;
+        // ---------------- the state: row m of R^T, half of the columns ----------------
+        const int sw = warp - LY::SW0, q = sw & 3, half = sw >> 2, m = product_row<D1>(q, lane);
+        const bool mine = product_lane<D1>(lane);
         constexpr int NC = D2 / 2;
         float r[NC];
         // (the entry state comes from the call's previous kernel; the other roles' inputs are older than the call)
         decay_wait();
-        const float *E = p.entry && m < p.d1
+        const float *E = p.entry && mine && m < p.d1
                              ? p.entry + (((long long)wk.b * p.H + wk.h) * p.nseg + wk.seg) * p.d1 * p.d2 : nullptr;
 #pragma unroll
         for (int c = 0; c < NC; c += 4) {
@@ -628,18 +690,16 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
                 // the previous chunk's write, and (issued before it) the last read of the bf16 state
                 if (!mbar_wait_suspend(&ds_full, (uint32_t)((i - 1) & 1), status, lim)) break;
                 fence_after_sync();
-                if (32 * q < D1) {
 #pragma unroll
-                    for (int c = 0; c < NC; c += 16) {
-                        float d[16];
-                        tmem_ld16(taddr(tb, 32 * q, LY::cD + half * NC + c), d);
-                        tmem_wait_ld();
+                for (int c = 0; c < NC; c += 16) {
+                    float d[16];
+                    tmem_ld16(taddr(tb, 32 * q, LY::cD + half * NC + c), d);
+                    tmem_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) r[c + k] = fmaf(an, r[c + k], d[k]);
-                    }
+                    for (int k = 0; k < 16; ++k) r[c + k] = fmaf(an, r[c + k], d[k]);
                 }
             }
-            if (32 * q < D1) {
+            if (mine) {
 #pragma unroll
                 for (int c = 0; c < NC; c += 8)
                     *reinterpret_cast<uint4 *>(sm + LY::R + sw128_off(m, half * NC + c, LY::R_BLK)) =
@@ -670,7 +730,10 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
             if (i > 0 && !mbar_wait_suspend(&yp_free, (uint32_t)((i - 1) & 1), status, lim)) break;
             if (i + 1 < wk.nch) {  // (nobody reads the state behind the last chunk)
                 fence_after_sync();
-                if (32 * q < D1) {
+                if constexpr (D1 == 64) {
+                    weigh_tile64<2>(s + LY::Y, sm + LY::YP, pw.w, n, yt, 32 * LY::YW);
+                    fence_async_smem();
+                } else {
 #pragma unroll 1
                     for (int j0 = 64 * half; j0 < 64 * half + 64; j0 += kWeigh)
                         weigh<2>(s + LY::Y, m, pw.w, j0, n, taddr(tb, 32 * q, 0), LY::cY);
