@@ -68,14 +68,16 @@ prism_status check_call(const prism_decay_shape *s, const void *q, const void *k
 }
 
 // Segments per sequence, for a launch of `passes` passes.  One CTA per SM walks one segment, chunk after
-// chunk, so a plan's time is about (waves of CTAs) x (chunks of a segment + what starting one costs, about
-// kStart chunks).
+// chunk; starting one costs about kStart chunks.  Full sequences: the time is about (waves of CTAs) x (chunks
+// of a segment + kStart).  A padded batch, whose lengths only the device knows, is taken to be half full: CTAs
+// behind their sequence's end leave at once, so the work spreads evenly and ends with one whole segment more.
+// (32 x 4 sequences of up to 8192 tokens, 64 wide, random lengths: one segment each 205 us, eight 174 us.)
 struct DecayPlan {
     int chunk, nseg, seg_tokens;
 };
 constexpr int kStart = 2;
 
-DecayPlan plan_of(const prism_decay_shape &s, int passes) {
+DecayPlan plan_of(const prism_decay_shape &s, int passes, bool padded) {
     const int chunk = s.io == PRISM_F32 ? kDecayChunkSimt : kDecayChunkTc;
     const int nch = std::max(1, (s.T + chunk - 1) / chunk);
     const long long ctas = std::max(1LL, (long long)s.B * s.H * passes);
@@ -84,7 +86,8 @@ DecayPlan plan_of(const prism_decay_shape &s, int passes) {
     long long least = 0;
     for (int want = 1; want <= std::min(nch, 128); ++want) {
         const int per = (nch + want - 1) / want, nseg = (nch + per - 1) / per;
-        const long long cost = (ctas * nseg + sms - 1) / sms * (per + kStart);
+        const long long cost = padded ? ctas * nseg * (per + kStart) / (2 * sms) + per + kStart
+                                      : (ctas * nseg + sms - 1) / sms * (per + kStart);
         if (want == 1 || cost < least) {
             least = cost;
             best = DecayPlan{chunk, nseg, per * chunk};
@@ -177,7 +180,7 @@ prism_status prism_decay_scan_fwd_workspace_size(const prism_decay_shape *shape,
     if (!bytes) return PRISM_ERR_INVALID_ARG;
     const prism_status st = check_shape(shape);
     if (st != PRISM_OK) return st;
-    *bytes = std::max<size_t>(256, sums_bytes(*shape, plan_of(*shape, 1)));
+    *bytes = std::max<size_t>(256, std::max(sums_bytes(*shape, plan_of(*shape, 1, false)), sums_bytes(*shape, plan_of(*shape, 1, true))));
     return PRISM_OK;
 }
 
@@ -199,7 +202,7 @@ prism_status prism_decay_scan_fwd(const prism_decay_shape *shape, const void *q,
                          {lengths, (size_t)s.B * 4}, {S_final == S0 ? nullptr : S0, state}};
     if (c.work && outputs_alias(outs, 3, ins, 6)) return PRISM_ERR_INVALID_ARG;
     if (s.B == 0 || s.H == 0) return PRISM_OK;
-    Runner r{s, plan_of(s, 1), decay, lengths, (cudaStream_t)stream};
+    Runner r{s, plan_of(s, 1, lengths != nullptr), decay, lengths, (cudaStream_t)stream};
     float *F = (float *)workspace;
     if (s.T == 0) {
         r.copy_state(S_final, S0);
@@ -219,7 +222,8 @@ prism_status prism_decay_scan_bwd_workspace_size(const prism_decay_shape *shape,
     if (!bytes) return PRISM_ERR_INVALID_ARG;
     const prism_status st = check_shape(shape);
     if (st != PRISM_OK) return st;
-    *bytes = std::max<size_t>(256, 2 * sums_bytes(*shape, plan_of(*shape, 3)) + shared_grad_bytes(*shape, shape->dk) +
+    *bytes = std::max<size_t>(256, 2 * std::max(sums_bytes(*shape, plan_of(*shape, 3, false)), sums_bytes(*shape, plan_of(*shape, 3, true))) +
+                                       shared_grad_bytes(*shape, shape->dk) +
                                        shared_grad_bytes(*shape, shape->dv));
     return PRISM_OK;
 }
@@ -246,7 +250,7 @@ prism_status prism_decay_scan_bwd(const prism_decay_shape *shape, const void *q,
                          {S0, state}, {dO, rows * s.H * s.dv}, {dS_final, state}};
     if (c.work && outputs_alias(outs, 5, ins, 8)) return PRISM_ERR_INVALID_ARG;
     if (s.B == 0 || s.H == 0) return PRISM_OK;
-    Runner r{s, plan_of(s, 3), decay, lengths, (cudaStream_t)stream};
+    Runner r{s, plan_of(s, 3, lengths != nullptr), decay, lengths, (cudaStream_t)stream};
     if (s.T == 0) {
         r.copy_state(dS0, dS_final);
     } else {

@@ -369,12 +369,10 @@ struct PassLayout {
     static constexpr uint32_t R_BLK = D1 * 128;
     static constexpr uint32_t YP = R + R_BLK * (D2 / 64), YP_BYTES = D1 == 64 ? 2 * kBlk : 0;  // the weighted Y (or in TMEM)
     static constexpr uint32_t BYTES = YP + YP_BYTES + 1024;
-    // TMEM columns: P twice where there is room, so that the next chunk's P is computed while this one's is weighted
-    // (not at 128 x 128: 2 x 128 for P, 128 each for the outputs, the write and the weighted Y)
-    static constexpr int NPB = D1 == 128 && D2 == 128 ? 1 : 2;
-    static constexpr uint32_t cP = 0, cO = NPB * 128, cD = cO + D2, cY = cD + D2;
+    // TMEM columns.  (A second P, for the next chunk's, where there is room for it: no faster at 64 x 64.)
+    static constexpr uint32_t cP = 0, cO = 128, cD = cO + D2, cY = cD + D2;
     static_assert(BYTES + 1024 <= 227 * 1024, "shared memory budget");
-    static_assert(cY + (D1 == 64 ? 0 : 128) <= 512, "TMEM columns");
+    static_assert(cY + 128 <= 512, "TMEM columns");
 };
 
 template <int D1, int D2>
@@ -387,7 +385,7 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     __shared__ uint64_t x_full[NST], y_full[NST], z_full[NST], x_free[NST], y_free[NST], z_free[NST];
-    __shared__ uint64_t p_full[LY::NPB], p_ready[LY::NPB], qs_full, o_scaled, o_full, o_free, s_ready, ds_full, yp_full, yp_free, drain;
+    __shared__ uint64_t p_full, p_ready, qs_full, o_scaled, o_full, o_free, s_ready, ds_full, yp_full, yp_free, drain;
     __shared__ Powers pw;
     __shared__ uint32_t tmem_base_sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -406,10 +404,8 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
             mbar_init(&y_free[i], LY::YW + 1);
             mbar_init(&z_free[i], LY::OW);
         }
-        for (int i = 0; i < LY::NPB; ++i) {
-            mbar_init(&p_full[i], 1);
-            mbar_init(&p_ready[i], LY::PW);
-        }
+        mbar_init(&p_full, 1);
+        mbar_init(&p_ready, LY::PW);
         mbar_init(&qs_full, 1);
         mbar_init(&o_scaled, LY::OW);
         mbar_init(&o_full, 1);
@@ -460,25 +456,18 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
             auto oy = [](int ks) { return 8 * ks; };
             auto op = [](int ks) { return 8 * ks + (ks >= 4 ? 32 : 0); };  // P': 64 tokens in each half of P
             const uint64_t dR = make_desc(smem_u32(sm + LY::R), LY::R_BLK, 1024, 2);
-            // P of chunk i (its region's last readers are products issued before)
-            auto issue_P = [&](int i) {
+            for (int i = 0; i < wk.nch; ++i) {
                 const int st = i % NST;
-                const uint32_t par = (uint32_t)((i / NST) & 1), s = smem_u32(sm + st * LY::STAGE);
-                if (!mbar_wait_suspend(&x_full[st], par, status, lim) || !mbar_wait_suspend(&y_full[st], par, status, lim)) return false;
-                fence_after_sync();
-                mma_steps_warp<D1 / 16>(tb + LY::cP + 128 * (i % LY::NPB), idP, make_desc(s + LY::X, 16, 1024, 2),
-                                        make_desc(s + LY::Y, 16, 1024, 2), ok_, ok_, false);
-                mma_commit_warp(&p_full[i % LY::NPB]);
-                mma_commit_warp(&y_free[st]);
-                return true;
-            };
-            bool go = LY::NPB == 1 || wk.nch == 0 || issue_P(0);
-            for (int i = 0; i < wk.nch && go; ++i) {
-                const int st = i % NST, pb = i % LY::NPB;
                 const uint32_t par = (uint32_t)((i / NST) & 1), ph = (uint32_t)(i & 1), before = (uint32_t)((i - 1) & 1);
                 const uint32_t s = smem_u32(sm + st * LY::STAGE);
-                const uint64_t dX = make_desc(s + LY::X, 16, 1024, 2), dZ = make_desc(s + LY::Z, kBlk, 1024, 2);
-                if (LY::NPB == 1 ? !issue_P(i) : i + 1 < wk.nch && !issue_P(i + 1)) break;
+                const uint64_t dX = make_desc(s + LY::X, 16, 1024, 2), dY = make_desc(s + LY::Y, 16, 1024, 2),
+                               dZ = make_desc(s + LY::Z, kBlk, 1024, 2);
+                if (!mbar_wait_suspend(&x_full[st], par, status, lim) || !mbar_wait_suspend(&y_full[st], par, status, lim)) break;
+                fence_after_sync();
+                // P (its region's last readers were the previous chunk's P' Z products, issued before)
+                mma_steps_warp<D1 / 16>(tb + LY::cP, idP, dX, dY, ok_, ok_, false);
+                mma_commit_warp(&p_full);
+                mma_commit_warp(&y_free[st]);
                 // X R^T
                 if (!mbar_wait_suspend(&s_ready, ph, status, lim) || (i > 0 && !mbar_wait_suspend(&o_free, before, status, lim))) break;
                 fence_after_sync();
@@ -501,9 +490,9 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
                     mma_commit_warp(&yp_free);
                 }
                 // O += P' Z
-                if (!mbar_wait_suspend(&p_ready[pb], (uint32_t)((i / LY::NPB) & 1), status, lim) || !mbar_wait_suspend(&o_scaled, ph, status, lim)) break;
+                if (!mbar_wait_suspend(&p_ready, ph, status, lim) || !mbar_wait_suspend(&o_scaled, ph, status, lim)) break;
                 fence_after_sync();
-                mma_steps_tmem_a_warp<CT / 16>(tb + LY::cO, idZ, tb + LY::cP + 128 * pb, dZ, op, omn, true);
+                mma_steps_tmem_a_warp<CT / 16>(tb + LY::cO, idZ, tb + LY::cP, dZ, op, omn, true);
                 mma_commit_warp(&o_full);
             }
             mma_commit_warp(&drain);
@@ -517,9 +506,9 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
         // two warps per 32 rows, 64 columns each, whose bf16 values go to the first 32 of the warp's own
         const int q = warp & 3, half = warp >> 2, row = 32 * q + lane;
         for (int i = 0; i < wk.nch; ++i) {
-            const int n = wk.n(i), pb = i % LY::NPB;
-            const uint32_t tl = taddr(tb, 32 * q, LY::cP + 128 * pb);
-            if (!mbar_wait_suspend(&p_full[pb], (uint32_t)((i / LY::NPB) & 1), status, lim)) break;
+            const int n = wk.n(i);
+            const uint32_t tl = taddr(tb, 32 * q, LY::cP);
+            if (!mbar_wait_suspend(&p_full, (uint32_t)(i & 1), status, lim)) break;
             fence_after_sync();
             // 16 columns at a time, in a loop: unrolled, the five roles' code of a chunk no longer fits the
             // instruction cache and every role waits for its instructions (P' took 7000 cycles instead of 1400)
@@ -569,7 +558,7 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
             tmem_wait_st();
             fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_ready[pb]);
+            if (lane == 0) mbar_arrive(&p_ready);
         }
     } else if (warp < LY::SW0) {
         setmaxnreg_dec<LY::RO>();
