@@ -27,6 +27,7 @@
 #include <stdint.h>
 
 #include "common.cuh"
+#include "dependent.cuh"
 
 namespace prism {
 
@@ -68,30 +69,6 @@ __device__ __forceinline__ float decay_pow(float a, int n) {
     for (; n > 0; n >>= 1, s *= s)
         if (n & 1) r *= s;
     return (float)r;
-}
-
-// Dependent launches: a kernel lets the next one of the call start once it has itself seen its predecessor
-// complete, so whatever a kernel reads before decay_wait() is older than the call.
-__device__ __forceinline__ void decay_wait() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
-// Launches `kern` so that its start may overlap the end of the call's previous kernel (`dependent`).
-template <typename... P, typename... A>
-cudaError_t decay_launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, bool dependent, const A &...args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = dependent ? 1 : 0;
-    launch_probe_mark(s);
-    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 // Passes (or segment sums) of one launch, all of the same B, H, T, lengths and segments: the CTAs of one

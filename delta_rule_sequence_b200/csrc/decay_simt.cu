@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(NT) decay_sum_simt_kernel(const __grid_constan
     extern __shared__ __align__(16) float sm[];
     using SZ = SumSizes<D1, D2>;
     float *pw = sm + SZ::NB * SZ::SET, *w = pw + CH + 1;
-    decay_wait();
+    dependent_wait();
     const DecayPass &p = set.p[blockIdx.x / set.p[0].nseg];
     const int seg = blockIdx.x % p.nseg, h = blockIdx.y, b = blockIdx.z;
     const int len = decay_len(p.lengths, b, p.T);
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(NT) decay_pass_simt_kernel(const __grid_consta
     constexpr int PP = CH + 4;
     using SZ = PassSizes<D1, D2>;
     float *R = sm + SZ::NB * SZ::SET, *P = R + D1 * (D2 + 4), *pw = P + CH * PP, *w = pw + CH + 1;
-    decay_wait();
+    dependent_wait();
     const DecayPass &p = set.p[blockIdx.x / set.p[0].nseg];
     const int seg = blockIdx.x % p.nseg, h = blockIdx.y, b = blockIdx.z;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -286,7 +286,7 @@ cudaError_t launch_one(const DecayPassSet &set, bool sum, cudaStream_t s) {
     auto kern = sum ? decay_sum_simt_kernel<D1, D2> : decay_pass_simt_kernel<D1, D2>;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (err != cudaSuccess) return err;
-    return decay_launch(kern, dim3(set.count * p.nseg, p.H, p.B), NT, bytes, s, set.dependent, set);
+    return dependent_launch(kern, dim3(set.count * p.nseg, p.H, p.B), NT, bytes, s, set.dependent, set);
 }
 
 // Four state elements per thread, walked over the segments in order: entry states replace the sums.  The
@@ -296,7 +296,7 @@ cudaError_t launch_one(const DecayPassSet &set, bool sum, cudaStream_t s) {
 constexpr int kAhead = 8;
 
 __global__ void __launch_bounds__(128) decay_carry_kernel(const __grid_constant__ DecayCarry c) {
-    decay_wait();
+    dependent_wait();
     const DecayCarryOne &o = c.c[blockIdx.z];
     __shared__ float pw[2];
     const int bh = blockIdx.x, e = 4 * (blockIdx.y * 128 + threadIdx.x);
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(128) decay_carry_kernel(const __grid_constant_
 
 template <typename IO>
 __global__ void decay_group_sum_kernel(DecayGroupSum a) {
-    decay_wait();
+    dependent_wait();
     const int which = blockIdx.y, d = a.d[which], div = a.div;
     const float *part = a.part[which];
     IO *out = (IO *)a.out[which];
@@ -358,13 +358,13 @@ cudaError_t launch_decay_simt(const DecayPassSet &set, bool sum, cudaStream_t s)
 }
 
 cudaError_t launch_decay_carry(const DecayCarry &c, cudaStream_t s) {
-    return decay_launch(decay_carry_kernel, dim3(c.BH, (c.elems + 511) / 512, c.count), 128, 0, s, c.dependent, c);
+    return dependent_launch(decay_carry_kernel, dim3(c.BH, (c.elems + 511) / 512, c.count), 128, 0, s, c.dependent, c);
 }
 
 cudaError_t launch_decay_group_sum(const DecayGroupSum &g, bool io_f32, cudaStream_t s) {
     const int d = g.d[0] > g.d[1] ? g.d[0] : g.d[1];
     const dim3 grid((unsigned)((g.groups * (d / 4) + 255) / 256), 2);
-    return decay_launch(io_f32 ? decay_group_sum_kernel<float> : decay_group_sum_kernel<__nv_bfloat16>, grid, 256, 0, s, true, g);
+    return dependent_launch(io_f32 ? decay_group_sum_kernel<float> : decay_group_sum_kernel<__nv_bfloat16>, grid, 256, 0, s, true, g);
 }
 
 }  // namespace prism

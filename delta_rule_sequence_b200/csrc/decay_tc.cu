@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
     __shared__ __align__(16) float w_last[CT];  // the weights of the walk's last chunk
     __shared__ uint32_t tmem_base_sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    decay_wait();
+    dependent_wait();
     const Walk wk(p);
     uint32_t *status = &g_decay_status;
     const uint32_t lim = p.stall ? kStallPolls : kPolls;
@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
         constexpr int NC = D2 / 2;
         float r[NC];
         // (the entry state comes from the call's previous kernel; the other roles' inputs are older than the call)
-        decay_wait();
+        dependent_wait();
         const float *E = p.entry && mine && m < p.d1
                              ? p.entry + (((long long)wk.b * p.H + wk.h) * p.nseg + wk.seg) * p.d1 * p.d2 : nullptr;
 #pragma unroll
@@ -784,7 +784,7 @@ cudaError_t launch_one(const DecayPassSet &set, bool sum, cudaStream_t s) {
         if (!sum && attr.numRegs * threads < PassLayout<D1, D2>::SHARES) return cudaErrorInvalidKernelImage;
         if (dev < 64) ready[sum][dev] = true;
     }
-    return decay_launch(kern, dim3(set.count * p.nseg, p.H, p.B), threads, bytes, s, set.dependent, set, maps);
+    return dependent_launch(kern, dim3(set.count * p.nseg, p.H, p.B), threads, bytes, s, set.dependent, set, maps);
 }
 
 }  // namespace

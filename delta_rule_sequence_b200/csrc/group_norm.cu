@@ -20,6 +20,7 @@
 
 #include "api.cuh"
 #include "common.cuh"
+#include "dependent.cuh"
 #include "f32x2.cuh"
 
 namespace prism {
@@ -318,6 +319,7 @@ template <typename IO, int V, int K, int LG, int MODE>
 __global__ void __launch_bounds__(kRowThreads, K == 1 ? kRowBwdBlocks : 1) norm_rows_bwd_kernel(NormArgs p, int row_lanes) {
     using U = Unit<V>;
     constexpr int NU = kUnits<V>;
+    dependent_wait();
     const RowLane<V, K, LG> t(p, row_lanes);
     const float inv = 1.f / (float)t.D;
     U sz[K][NU], szx[K][NU];
@@ -431,6 +433,7 @@ __global__ void __launch_bounds__(kRowThreads, K == 1 ? kRowBwdBlocks : 1) norm_
 __global__ void __launch_bounds__(1024) norm_channel_sum_kernel(const float *parts, int n, int C, float *dweight, float *dbias) {
     __shared__ float s[32][33];
     const int lane = threadIdx.x & 31, k = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+    dependent_wait();
     float acc[4] = {};
     if (col < 2 * C)
         for (int i = k; i < n; i += 128)
@@ -501,6 +504,7 @@ __host__ __device__ inline int norm_pieces(int G, int blocks) { return G + block
 template <typename IO, int V>
 __global__ void __launch_bounds__(kTileThreads, 2) norm_tile_stats_kernel(NormArgs p) {
     __shared__ float sh_mean[kTileThreads * V], sh_m2[kTileThreads * V];
+    dependent_wait();
     const Tile<V> t(p, blockIdx.x);
     const int D = p.C / p.G;
     float mean[V] = {}, m2[V] = {};
@@ -591,6 +595,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) norm_tile_apply_kernel(NormAr
     __shared__ float sh_mean[kTileCols * V], sh_rstd[kTileCols * V];
     const Tile<V> t(p, blockIdx.x);
     const int D = p.C / p.G, g0 = t.first_group(D);
+    dependent_wait();
     for (int g = g0 + kGroupsAtOnce * (threadIdx.x >> 5); g <= t.last_group(D); g += kGroupsAtOnce * (kTileThreads / 32)) {
         Stat st[kGroupsAtOnce] = {};
         visit_pieces<V>(p, t.n, g, t.last_group(D), gridDim.y,
@@ -647,6 +652,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) norm_tile_grad_sums_kernel(No
     __shared__ float sh1[kTileThreads * V], sh2[kTileThreads * V];
     __shared__ float tot1[kTileCols * V], tot2[kTileCols * V];
     const int D = p.C / p.G;
+    dependent_wait();
     for (int i = threadIdx.x; i < kTileCols * V; i += kTileThreads) tot1[i] = tot2[i] = 0.f;
     for (int unit = blockIdx.x; unit < p.N * p.tiles; unit += gridDim.x) {
         const Tile<V> t(p, unit);
@@ -736,6 +742,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) norm_tile_grad_apply_kernel(N
     __shared__ float sh1[kTileCols * V], sh2[kTileCols * V];
     const Tile<V> t(p, blockIdx.x);
     const int D = p.C / p.G, g0 = t.first_group(D), lane = threadIdx.x & 31;
+    dependent_wait();
     const float inv = 1.f / ((float)D * (float)p.S);
     for (int g = g0 + kGroupsAtOnce * (threadIdx.x >> 5); g <= t.last_group(D); g += kGroupsAtOnce * (kTileThreads / 32)) {
         float2 sum[kGroupsAtOnce] = {};
@@ -885,15 +892,17 @@ cudaError_t launch_fwd(const NormArgs &a, const NormPlan &pl, cudaStream_t s) {
     }
     const dim3 grid(a.N * a.tiles, pl.col_blocks);
     (pl.V == 1 ? norm_tile_stats_kernel<IO, 1> : norm_tile_stats_kernel<IO, F>)<<<grid, kTileThreads, 0, s>>>(a);
-    launch_probe_mark(s);
-    if (pl.V == 1) norm_tile_apply_kernel<IO, 1, kRuntime><<<grid, kTileThreads, 0, s>>>(a);
-    else with_mode(a, [&](auto m) { norm_tile_apply_kernel<IO, F, m.value><<<grid, kTileThreads, 0, s>>>(a); });
-    return cudaGetLastError();
+    cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    if (pl.V == 1) err = dependent_launch(norm_tile_apply_kernel<IO, 1, kRuntime>, grid, kTileThreads, 0, s, true, a);
+    else with_mode(a, [&](auto m) { err = dependent_launch(norm_tile_apply_kernel<IO, F, m.value>, grid, kTileThreads, 0, s, true, a); });
+    return err;
 }
 
 template <typename IO>
 cudaError_t launch_bwd(const NormArgs &a, const NormPlan &pl, float *dweight, float *dbias, cudaStream_t s) {
     constexpr int F = 16 / sizeof(IO);
+    cudaError_t err = cudaSuccess;
     launch_probe_mark(s);
     if (pl.rows) {
         with_lanes(pl.LG, [&](auto l) {
@@ -907,15 +916,15 @@ cudaError_t launch_bwd(const NormArgs &a, const NormPlan &pl, float *dweight, fl
         const dim3 grid(a.N * a.tiles, pl.col_blocks);
         if (pl.V == 1) norm_tile_grad_sums_kernel<IO, 1, kRuntime><<<dim3(a.parts, pl.col_blocks), kTileThreads, 0, s>>>(a);
         else with_mode(a, [&](auto m) { norm_tile_grad_sums_kernel<IO, F, m.value><<<dim3(a.parts, pl.col_blocks), kTileThreads, 0, s>>>(a); });
-        launch_probe_mark(s);
-        if (pl.V == 1) norm_tile_grad_apply_kernel<IO, 1, kRuntime><<<grid, kTileThreads, 0, s>>>(a);
-        else with_mode(a, [&](auto m) { norm_tile_grad_apply_kernel<IO, F, m.value><<<grid, kTileThreads, 0, s>>>(a); });
+        if ((err = cudaGetLastError()) != cudaSuccess) return err;
+        if (pl.V == 1) err = dependent_launch(norm_tile_grad_apply_kernel<IO, 1, kRuntime>, grid, kTileThreads, 0, s, true, a);
+        else with_mode(a, [&](auto m) { err = dependent_launch(norm_tile_grad_apply_kernel<IO, F, m.value>, grid, kTileThreads, 0, s, true, a); });
     }
-    if (dweight || dbias) {
-        launch_probe_mark(s);
-        norm_channel_sum_kernel<<<(2 * a.C + 31) / 32, 1024, 0, s>>>(a.chan_parts, a.parts, a.C, dweight, dbias);
-    }
-    return cudaGetLastError();
+    if (err == cudaSuccess) err = cudaGetLastError();
+    if (err == cudaSuccess && (dweight || dbias))
+        err = dependent_launch(norm_channel_sum_kernel, dim3((2 * a.C + 31) / 32), 1024, 0, s, true, (const float *)a.chan_parts, a.parts,
+                               a.C, dweight, dbias);
+    return err;
 }
 
 NormArgs args_of(const prism_norm_shape &s, const NormPlan &pl, const void *x, const float *weight, const float *bias,
@@ -940,7 +949,7 @@ prism_status prism_group_norm_fwd_workspace_size(const prism_norm_shape *shape, 
     if (!bytes) return PRISM_ERR_INVALID_ARG;
     const prism_status st = check_shape(shape);
     if (st != PRISM_OK) return st;
-    *bytes = std::max<size_t>(256, stat_bytes(*shape, plan_of(*shape, false)));
+    *bytes = shape->N == 0 || shape->S == 0 ? 0 : stat_bytes(*shape, plan_of(*shape, false));
     return PRISM_OK;
 }
 
@@ -955,8 +964,8 @@ prism_status prism_group_norm_fwd(const prism_norm_shape *shape, const void *x, 
     if (!x || !y || !aligned16(x) || !aligned16(y) || !aligned16(gate)) return PRISM_ERR_INVALID_ARG;
     if (!aligned4(weight) || !aligned4(bias) || !aligned4(mean) || !aligned4(rstd)) return PRISM_ERR_INVALID_ARG;
     const NormPlan pl = plan_of(s, false);
-    const size_t need = std::max<size_t>(256, stat_bytes(s, pl));
-    if (!workspace || ws_bytes < need || ((uintptr_t)workspace & 255u)) return PRISM_ERR_INVALID_ARG;
+    const size_t need = stat_bytes(s, pl);
+    if (need > 0 && (!workspace || ws_bytes < need || ((uintptr_t)workspace & 255u))) return PRISM_ERR_INVALID_ARG;
     const ByteRange outs[] = {{y, n}, {mean, groups}, {rstd, groups}, {workspace, need}};
     const ByteRange ins[] = {{x, n}, {gate, n}, {weight, (size_t)s.C * 4}, {bias, (size_t)s.C * 4}};
     if (outputs_alias(outs, 4, ins, 4)) return PRISM_ERR_INVALID_ARG;

@@ -498,13 +498,18 @@ def _scratch_bytes(entry, shape_type, fields, device_index) -> int:
     return need.value
 
 
-def _scratch(entry, shape, fields, device, workspace) -> torch.Tensor:
-    """The caller's workspace, or a new one from torch's allocator: it belongs to this call alone, so
+def _scratch(entry, shape, fields, device, workspace):
+    """The caller's workspace, or (None where the call needs none) a new one from torch's allocator: it belongs to this call alone, so
     calls on several streams, and captured graphs, never share one."""
     if workspace is not None:
         _check_tensor("workspace", workspace, torch.uint8, (workspace.numel(),), device)
         return workspace
-    return torch.empty(_scratch_bytes(entry, type(shape), fields, device.index), dtype=torch.uint8, device=device)
+    need = _scratch_bytes(entry, type(shape), fields, device.index)
+    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+
+
+def _size(workspace) -> int:
+    return 0 if workspace is None else workspace.numel()
 
 
 def _launched_on(stream, device, *tensors) -> None:
@@ -595,7 +600,7 @@ def prism_decay_scan_fwd(q, k, v, decay, S0=None, lengths=None, *, o=None, S_fin
     _check_tensor("S_final", S_final, f32, (B, H, dv, dk), dev)
     ws = _scratch("prism_decay_scan_fwd_workspace_size", shape, sizes, dev, workspace)
     rc = _call(dev, lib.prism_decay_scan_fwd, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(S0),
-               _ptr(lengths), _ptr(o), _ptr(S_final), _ptr(ws), ctypes.c_size_t(ws.numel()), _stream(stream, dev))
+               _ptr(lengths), _ptr(o), _ptr(S_final), _ptr(ws), _size(ws), _stream(stream, dev))
     if rc != PRISM_OK:
         raise PrismError(rc, "prism_decay_scan_fwd")
     _launched_on(stream, dev, o, S_final, ws)
@@ -624,7 +629,7 @@ def prism_decay_scan_bwd(q, k, v, decay, S0=None, lengths=None, *, dO, dS_final=
     ws = _scratch("prism_decay_scan_bwd_workspace_size", shape, sizes, dev, workspace)
     rc = _call(dev, lib.prism_decay_scan_bwd, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(S0),
                _ptr(lengths), _ptr(dO), _ptr(dS_final), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
-               _ptr(out["dS0"]), _ptr(ws), ctypes.c_size_t(ws.numel()), _stream(stream, dev))
+               _ptr(out["dS0"]), _ptr(ws), _size(ws), _stream(stream, dev))
     if rc != PRISM_OK:
         raise PrismError(rc, "prism_decay_scan_bwd")
     _launched_on(stream, dev, ws, *out.values())
@@ -690,11 +695,10 @@ def prism_group_norm_fwd(x, groups, weight=None, bias=None, gate=None, *, eps=1e
     if y is None:
         y = torch.empty_like(x)
     _check_tensor("y", y, io, x.shape, dev)
-    mean = torch.empty((sizes[0], groups), dtype=torch.float32, device=dev)
-    rstd = torch.empty_like(mean)
+    mean, rstd = torch.empty((2, sizes[0], groups), dtype=torch.float32, device=dev).unbind(0)
     ws = _scratch("prism_group_norm_fwd_workspace_size", shape, sizes, dev, workspace)
     rc = _call(dev, lib.prism_group_norm_fwd, ctypes.byref(shape), _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate),
-               _ptr(y), _ptr(mean), _ptr(rstd), _ptr(ws), ctypes.c_size_t(ws.numel()), _stream(stream, dev))
+               _ptr(y), _ptr(mean), _ptr(rstd), _ptr(ws), _size(ws), _stream(stream, dev))
     if rc != PRISM_OK:
         raise PrismError(rc, "prism_group_norm_fwd")
     _launched_on(stream, dev, y, mean, rstd, ws)
@@ -724,7 +728,7 @@ def prism_group_norm_bwd(x, groups, mean, rstd, weight=None, bias=None, gate=Non
     ws = _scratch("prism_group_norm_bwd_workspace_size", shape, sizes, dev, workspace)
     rc = _call(dev, lib.prism_group_norm_bwd, ctypes.byref(shape), _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate),
                _ptr(mean), _ptr(rstd), _ptr(dy), _ptr(out["dx"]), _ptr(out.get("dgate")), _ptr(out.get("dweight")),
-               _ptr(out.get("dbias")), _ptr(ws), ctypes.c_size_t(ws.numel()), _stream(stream, dev))
+               _ptr(out.get("dbias")), _ptr(ws), _size(ws), _stream(stream, dev))
     if rc != PRISM_OK:
         raise PrismError(rc, "prism_group_norm_bwd")
     _launched_on(stream, dev, ws, *out.values())

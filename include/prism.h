@@ -358,7 +358,7 @@ prism_status prism_group_norm_fwd_workspace_size(const prism_norm_shape *shape, 
  *   y            [N,S,C] io         output
  *   mean, rstd   [N,G] fp32         outputs for prism_group_norm_bwd, each may be NULL
  *   workspace, ws_bytes             at least prism_group_norm_fwd_workspace_size bytes, 256-byte
- *                                   aligned; needs no clearing
+ *                                   aligned; needs no clearing; may be NULL where the size is 0
  * x, gate and y dense and 16-byte aligned, the others 4-byte aligned; no output may overlap an
  * input or another output.  C <= 2^20, N <= 2^24, N*G < 2^31.  All arithmetic in fp32, y rounded
  * once.  With N or S of zero nothing is written.
