@@ -30,7 +30,7 @@ bool make_operand(const prism_decay_shape &s, const void *p, const long long (&s
     long long r[3], last = d;
     for (int i = 0; i < 3; ++i) {
         r[i] = is_dense || n[i] <= 1 ? dense[i] : st[i];
-        if (n[i] > 1 && s.T > 0 && (r[i] <= 0 || r[i] % unit || r[i] >= (1LL << 40) / 4)) return false;
+        if (n[i] > 1 && s.T > 0 && (r[i] <= 0 || r[i] % unit || r[i] >= 1LL << 36)) return false;
         if (n[i] > 1) last += (n[i] - 1) * r[i];
     }
     out->t = DecayTensor{p, r[0], r[1], r[2], heads > 0 ? s.H / heads : 1};
@@ -49,7 +49,7 @@ prism_status check_shape(const prism_decay_shape *s) {
     if (s->io != PRISM_BF16 && s->io != PRISM_F32) return PRISM_ERR_INVALID_ARG;
     if (s->H > 0 && (s->Hkv < 1 || s->H % s->Hkv)) return PRISM_ERR_INVALID_ARG;
     if (!width_ok(s->dk) || !width_ok(s->dv)) return PRISM_ERR_UNSUPPORTED;
-    if (s->B > 65535 || s->H > 65535 || (long long)s->B * s->H > (1 << 24)) return PRISM_ERR_UNSUPPORTED;
+    if (s->B > 65535 || s->H > 65535 || (long long)s->B * s->H > (1 << 24) || s->T > (1 << 26)) return PRISM_ERR_UNSUPPORTED;
     return PRISM_OK;
 }
 

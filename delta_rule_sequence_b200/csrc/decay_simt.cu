@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(NT) decay_pass_simt_kernel(const __grid_consta
     }
     // rows behind the sequence's last token
     const int z0 = max(s0, s1);
-    for (int e = threadIdx.x; e < (send - z0) * p.d2; e += NT) ((float *)p.o)[(((long long)b * p.T + z0 + e / p.d2) * p.H + h) * p.d2 + e % p.d2] = 0.f;
+    for (long long e = threadIdx.x; e < (long long)(send - z0) * p.d2; e += NT) ((float *)p.o)[(((long long)b * p.T + z0 + e / p.d2) * p.H + h) * p.d2 + e % p.d2] = 0.f;
 }
 
 template <int D1, int D2>

@@ -740,7 +740,7 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
     // rows behind the sequence's last token
     const int z0 = max(wk.s0, wk.s1);
     const int row_bytes = p.d2 * (p.o_f32 ? 4 : 2), per_row = row_bytes / 16;
-    for (int e = tid; e < (wk.send - z0) * per_row; e += LY::THREADS) {
+    for (long long e = tid; e < (long long)(wk.send - z0) * per_row; e += LY::THREADS) {
         const long long t = z0 + e / per_row;
         *reinterpret_cast<uint4 *>((uint8_t *)p.o + (((long long)wk.b * p.T + t) * p.H + wk.h) * row_bytes + (e % per_row) * 16) =
             make_uint4(0, 0, 0, 0);

@@ -7,6 +7,7 @@ library is missing or the tensors are not on a CUDA device, the call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -512,13 +513,28 @@ def _size(workspace) -> int:
     return 0 if workspace is None else workspace.numel()
 
 
-def _launched_on(stream, device, *tensors) -> None:
-    """Tensors that a call allocated and that its kernels use on another stream than the current one:
-    their memory is not handed out again before that stream has passed the call."""
-    if stream is not None and stream != torch.cuda.current_stream(device):
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _allocating_on(stream, device):
+    """Context in which a call allocates: with the caller's stream current, so that the memory comes from that
+    stream's pool (memory that the current stream freed may still be in use there)."""
+    if stream is None or stream == torch.cuda.current_stream(device):
+        return _HERE
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+    return torch.cuda.stream(stream)
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _handed_out(stream, device, *tensors) -> None:
+    """Results made on another stream than the current one: the current one, where the caller is going to use
+    them, keeps their memory from being handed out again too early."""
+    if stream is not None:
+        here = torch.cuda.current_stream(device)
+        if stream != here:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(here)
 
 
 def _view_strides(name, x, dtype, shape, device):
@@ -592,18 +608,19 @@ def prism_decay_scan_fwd(q, k, v, decay, S0=None, lengths=None, *, o=None, S_fin
     f32 = torch.float32
     _check_tensor("S0", S0, f32, (B, H, dv, dk), dev)
     _check_tensor("lengths", lengths, torch.int32, (B,), dev)
-    if o is None:
-        o = torch.empty((B, T, H, dv), dtype=io, device=dev)
+    with _allocating_on(stream, dev):
+        if o is None:
+            o = torch.empty((B, T, H, dv), dtype=io, device=dev)
+        if S_final is None and want_state:
+            S_final = torch.empty((B, H, dv, dk), dtype=f32, device=dev)
+        ws = _scratch("prism_decay_scan_fwd_workspace_size", shape, sizes, dev, workspace)
     _check_tensor("o", o, io, (B, T, H, dv), dev)
-    if S_final is None and want_state:
-        S_final = torch.empty((B, H, dv, dk), dtype=f32, device=dev)
     _check_tensor("S_final", S_final, f32, (B, H, dv, dk), dev)
-    ws = _scratch("prism_decay_scan_fwd_workspace_size", shape, sizes, dev, workspace)
     rc = _call(dev, lib.prism_decay_scan_fwd, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(S0),
                _ptr(lengths), _ptr(o), _ptr(S_final), _ptr(ws), _size(ws), _stream(stream, dev))
     if rc != PRISM_OK:
         raise PrismError(rc, "prism_decay_scan_fwd")
-    _launched_on(stream, dev, o, S_final, ws)
+    _handed_out(stream, dev, o, S_final)
     return o, S_final
 
 
@@ -622,17 +639,18 @@ def prism_decay_scan_bwd(q, k, v, decay, S0=None, lengths=None, *, dO, dS_final=
         raise TypeError("dO must be a CUDA tensor (libprism has no CPU path)")
     _check_tensor("dO", dO, io, (B, T, H, dv), dev)
     _check_tensor("dS_final", dS_final, f32, (B, H, dv, dk), dev)
-    out = {"dq": torch.empty((B, T, H, dk), dtype=io, device=dev),
-           "dk": torch.empty((B, T, Hkv, dk), dtype=io, device=dev),
-           "dv": torch.empty((B, T, Hkv, dv), dtype=io, device=dev),
-           "dS0": torch.empty((B, H, dv, dk), dtype=f32, device=dev) if want_dS0 else None}
-    ws = _scratch("prism_decay_scan_bwd_workspace_size", shape, sizes, dev, workspace)
+    with _allocating_on(stream, dev):
+        out = {"dq": torch.empty((B, T, H, dk), dtype=io, device=dev),
+               "dk": torch.empty((B, T, Hkv, dk), dtype=io, device=dev),
+               "dv": torch.empty((B, T, Hkv, dv), dtype=io, device=dev),
+               "dS0": torch.empty((B, H, dv, dk), dtype=f32, device=dev) if want_dS0 else None}
+        ws = _scratch("prism_decay_scan_bwd_workspace_size", shape, sizes, dev, workspace)
     rc = _call(dev, lib.prism_decay_scan_bwd, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(S0),
                _ptr(lengths), _ptr(dO), _ptr(dS_final), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
                _ptr(out["dS0"]), _ptr(ws), _size(ws), _stream(stream, dev))
     if rc != PRISM_OK:
         raise PrismError(rc, "prism_decay_scan_bwd")
-    _launched_on(stream, dev, ws, *out.values())
+    _handed_out(stream, dev, *out.values())
     return out
 
 
@@ -646,13 +664,14 @@ def prism_decay_step(q, k, v, decay, S, *, o=None, stream=None):
         raise TypeError("S must be a CUDA tensor (libprism has no CPU path)")
     _check_tensor("S", S, torch.float32, (B, H, dv, dk), dev)
     if o is None:
-        o = torch.empty((B, T, H, dv), dtype=io, device=dev)
+        with _allocating_on(stream, dev):
+            o = torch.empty((B, T, H, dv), dtype=io, device=dev)
     _check_tensor("o", o, io, (B, T, H, dv), dev)
     rc = _call(dev, lib.prism_decay_step, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(S),
                _ptr(o), _stream(stream, dev))
     if rc != PRISM_OK:
         raise PrismError(rc, "prism_decay_step")
-    _launched_on(stream, dev, o)
+    _handed_out(stream, dev, o)
     return o
 
 
@@ -692,16 +711,17 @@ def prism_group_norm_fwd(x, groups, weight=None, bias=None, gate=None, *, eps=1e
     fp32 for prism_group_norm_bwd."""
     lib = load_library()
     shape, sizes, dev, io = _norm_inputs(x, groups, weight, bias, gate, eps, activation)
-    if y is None:
-        y = torch.empty_like(x)
+    with _allocating_on(stream, dev):
+        if y is None:
+            y = torch.empty_like(x)
+        mean, rstd = torch.empty((2, sizes[0], groups), dtype=torch.float32, device=dev).unbind(0)
+        ws = _scratch("prism_group_norm_fwd_workspace_size", shape, sizes, dev, workspace)
     _check_tensor("y", y, io, x.shape, dev)
-    mean, rstd = torch.empty((2, sizes[0], groups), dtype=torch.float32, device=dev).unbind(0)
-    ws = _scratch("prism_group_norm_fwd_workspace_size", shape, sizes, dev, workspace)
     rc = _call(dev, lib.prism_group_norm_fwd, ctypes.byref(shape), _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate),
                _ptr(y), _ptr(mean), _ptr(rstd), _ptr(ws), _size(ws), _stream(stream, dev))
     if rc != PRISM_OK:
         raise PrismError(rc, "prism_group_norm_fwd")
-    _launched_on(stream, dev, y, mean, rstd, ws)
+    _handed_out(stream, dev, y, mean, rstd)
     return y, mean, rstd
 
 
@@ -718,18 +738,19 @@ def prism_group_norm_bwd(x, groups, mean, rstd, weight=None, bias=None, gate=Non
     _check_tensor("mean", mean, f32, (sizes[0], groups), dev)
     _check_tensor("rstd", rstd, f32, (sizes[0], groups), dev)
     _check_tensor("dy", dy, io, x.shape, dev)
-    out = {"dx": torch.empty_like(x)}
-    if gate is not None:
-        out["dgate"] = torch.empty_like(x)
-    if weight is not None:
-        out["dweight"] = torch.empty_like(weight)
-    if bias is not None:
-        out["dbias"] = torch.empty_like(bias)
-    ws = _scratch("prism_group_norm_bwd_workspace_size", shape, sizes, dev, workspace)
+    with _allocating_on(stream, dev):
+        out = {"dx": torch.empty_like(x)}
+        if gate is not None:
+            out["dgate"] = torch.empty_like(x)
+        if weight is not None:
+            out["dweight"] = torch.empty_like(weight)
+        if bias is not None:
+            out["dbias"] = torch.empty_like(bias)
+        ws = _scratch("prism_group_norm_bwd_workspace_size", shape, sizes, dev, workspace)
     rc = _call(dev, lib.prism_group_norm_bwd, ctypes.byref(shape), _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate),
                _ptr(mean), _ptr(rstd), _ptr(dy), _ptr(out["dx"]), _ptr(out.get("dgate")), _ptr(out.get("dweight")),
                _ptr(out.get("dbias")), _ptr(ws), _size(ws), _stream(stream, dev))
     if rc != PRISM_OK:
         raise PrismError(rc, "prism_group_norm_bwd")
-    _launched_on(stream, dev, ws, *out.values())
+    _handed_out(stream, dev, *out.values())
     return out

@@ -80,27 +80,48 @@ class ChunkCounter:
         return S
 
 
+def head_norm(weight=None, bias=None, *, eps=1e-5, activation="silu"):
+    """The norm behind a scan, as a StreamingScan's norm_fn: every token's outputs normalised per head
+    (``prism_group_norm_fwd`` with one group per head), scaled by weight and bias [H * dv] fp32, then
+    through the activation, or multiplied by the gate's activation."""
+
+    def norm(o, gate):
+        from delta_rule_sequence_b200 import prism
+
+        B, c, H, dv = o.shape
+        flat = None if gate is None else gate.reshape(B * c, H * dv)
+        y, _, _ = prism.prism_group_norm_fwd(o.view(B * c, H * dv), H, weight, bias, flat, eps=eps,
+                                             activation=activation)
+        return y.view(B, c, H, dv)
+
+    return norm
+
+
 class StreamingScan:
     """Chunk-by-chunk inference: outputs of each arriving chunk from the current prefix state,
     then the chunk's element pushed into the counter.  Inputs per chunk as for prism_scan_fwd
-    ([B, c, H, ...] device tensors of the chunk's tokens); S0 the state before the stream."""
+    ([B, c, H, ...] device tensors of the chunk's tokens); S0 the state before the stream;
+    norm_fn(o, gate), for example head_norm(...), is applied to each chunk's outputs."""
 
     def __init__(self, S0=None, *, chunk=64, element_fn=None, compose_fn=None, fold_fn=None,
-                 scan_fn=None):
+                 scan_fn=None, norm_fn=None):
         if None in (element_fn, compose_fn, fold_fn, scan_fn):
             e, c, f, s = _library_steps()
             element_fn, compose_fn, fold_fn, scan_fn = (element_fn or e, compose_fn or c,
                                                         fold_fn or f, scan_fn or s)
         self.element, self.scan, self.chunk = element_fn, scan_fn, chunk
-        self.S0 = S0
+        self.S0, self.norm = S0, norm_fn
         self.counter = ChunkCounter(compose_fn, fold_fn)
 
-    def step(self, q, k, v, alpha, beta, u=None, w=None):
-        """Process one chunk: returns its outputs o [B, c, H, dv]."""
+    def step(self, q, k, v, alpha, beta, u=None, w=None, gate=None):
+        """Process one chunk: returns its outputs [B, c, H, dv], normalised (with the gate, like the
+        outputs, or None) where the stream has a norm_fn."""
+        if gate is not None and self.norm is None:
+            raise ValueError("a gate needs a stream with a norm_fn")
         entry = self.counter.state(self.S0)
         o, _ = self.scan(q, k, v, alpha, beta, u, w, entry, self.chunk)
         self.counter.push(self.element(q, k, v, alpha, beta, u, w, self.chunk))
-        return o
+        return o if self.norm is None else self.norm(o, gate)
 
     def state(self):
         """The state after every chunk so far."""

@@ -258,7 +258,8 @@ typedef struct {
     prism_dtype io;   /* type of q, k, v, o and of their gradients (decay and states are fp32)    */
     /* Elements between consecutive batches, tokens and heads of q, k and v (unit stride along the
      * width), so that views of a fused projection need no copy.  All three zero: dense.  Strides
-     * along an extent of 0 or 1 are ignored; the others are positive multiples of 16 bytes.       */
+     * along an extent of 0 or 1 are ignored; the others are positive multiples of 16 bytes below
+     * 2^36 elements.                                                                              */
     long long q_stride[3], k_stride[3], v_stride[3];
 } prism_decay_shape;
 
@@ -280,7 +281,8 @@ prism_status prism_decay_scan_fwd_workspace_size(const prism_decay_shape *shape,
  *                                  S_final == S0 is allowed
  *   workspace, ws_bytes            at least prism_decay_scan_fwd_workspace_size bytes, 256-byte
  *                                  aligned; needs no clearing, and nothing in it outlives the call
- * No other overlap of an output with an input or output is allowed.  B, H <= 65535 and B*H <= 2^24.
+ * No other overlap of an output with an input or output is allowed.  B, H <= 65535, B*H <= 2^24,
+ * T <= 2^26.
  * States and sums are fp32.  bf16 outputs are rounded to nearest even; inside, the products of a
  * chunk and the state are rounded to bf16 once where they enter an output's product, never where
  * they enter a state.  A non-finite value in a valid token reaches outputs of its whole 128-token

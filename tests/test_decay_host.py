@@ -51,7 +51,7 @@ def bwd(lib, s, **kw):
 @pytest.mark.parametrize("kw,want", [
     (dict(dk=48), UNSUPPORTED), (dict(dv=256), UNSUPPORTED), (dict(dk=0), INVALID), (dict(T=-1), INVALID),
     (dict(B=-1), INVALID), (dict(Hkv=3), INVALID), (dict(Hkv=0), INVALID), (dict(io=2), INVALID),
-    (dict(B=70000), UNSUPPORTED), (dict(H=65536, Hkv=1), UNSUPPORTED), (dict(B=60000, H=400), UNSUPPORTED),
+    (dict(T=(1 << 26) + 1), UNSUPPORTED), (dict(q=(1 << 36, 256, 64)), INVALID), (dict(B=70000), UNSUPPORTED), (dict(H=65536, Hkv=1), UNSUPPORTED), (dict(B=60000, H=400), UNSUPPORTED),
     (dict(q=(25600, 256, 60)), INVALID),    # a head stride that is no multiple of 16 bytes
     (dict(k=(12800, 0, 64)), INVALID),      # every token the same key
     (dict(v=(-6400, 64, 32)), INVALID),
@@ -60,7 +60,7 @@ def test_decay_scan_refuses_shapes(lib, kw, want):
     s = shape(**kw)
     assert fwd(lib, s, ws_bytes=1 << 40) == want
     assert bwd(lib, s) == want
-    if not {"T", "k"} & set(kw):  # (a token stride of zero is fine where there is one token)
+    if not {"T", "k", "q"} & set(kw):  # (a token stride of zero is fine where there is one token)
         assert lib.prism_decay_step(ctypes.byref(shape(T=1, **kw)), *[ptr(i) for i in range(6)], None) == want
 
 

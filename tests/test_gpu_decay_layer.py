@@ -119,3 +119,47 @@ def test_autograd_through_the_layer():
     # once more each, two roundings inside: below 6 x 2^-8
     for a, b in zip(eager, want):
         assert (a.double() - b).norm() <= 6 * 2.0 ** -8 * b.norm()
+
+
+def test_streaming_with_the_output_norm():
+    """The chunk stream's outputs through the gated per-head norm, against the oracles of both; and the same
+    layer on the decay scan, whose chunks chain through S_final."""
+    import oracle
+    from delta_rule_sequence_b200.stream import StreamingScan, head_norm
+    from delta_rule_sequence_b200.workloads import WORKLOADS, make_inputs
+
+    P = prism()
+    wl = WORKLOADS["gdn"].with_(B=2, H=2, T=3 * 64, s0_std=0.02)
+    x = make_inputs(wl, seed=3)
+    d = {n: None if t is None else t.cuda() for n, t in x.items()}
+    g = torch.Generator().manual_seed(5)
+    gate = torch.randn(2, wl.T, 2, 128, generator=g).bfloat16().cuda()
+    w = (1 + 0.2 * torch.randn(256, generator=g)).cuda()
+    s = StreamingScan(d["S0"], norm_fn=head_norm(w))
+    plain = StreamingScan(d["S0"])
+    raw, outs = [], []
+    for t in range(0, wl.T, 64):
+        c = {n: None if v is None or n == "S0" else v[:, t:t + 64].contiguous() for n, v in d.items()}
+        args = (c["q"], c["k"], c["v"], c["alpha"], c["beta"])
+        outs.append(s.step(*args, gate=gate[:, t:t + 64]))
+        raw.append(plain.step(*args))
+    torch.cuda.synchronize()
+    o_ref, _ = oracle.scan_ref(**x)
+    raw = torch.cat(raw, 1)
+    err = np.abs(raw.double().cpu().numpy() - o_ref)
+    assert (err <= 2e-2 * (1 + np.abs(o_ref))).all()
+    y_ref, _, _ = group_norm_ref(raw.reshape(-1, 1, 256), 2, w, None, gate.reshape(-1, 1, 256), activation="silu")
+    y = torch.cat(outs, 1).double().cpu().numpy().reshape(y_ref.shape)
+    assert np.linalg.norm(y - y_ref) <= 2.0 ** -8 * np.linalg.norm(y_ref)  # rounded once
+
+    a = torch.tensor([0.9, 0.99], device="cuda")
+    whole, S_whole = P.prism_decay_scan_fwd(d["q"], d["k"], d["v"], a, d["S0"])
+    S, parts = d["S0"], []
+    for t in range(0, wl.T, 64):
+        o, S = P.prism_decay_scan_fwd(d["q"][:, t:t + 64], d["k"][:, t:t + 64], d["v"][:, t:t + 64], a, S)
+        parts.append(o)
+    torch.cuda.synchronize()
+    o_ref, S_ref = decay_scan_ref(d["q"], d["k"], d["v"], a, d["S0"])
+    for got, ref, lim in ((whole, o_ref, 2.0 ** -7), (torch.cat(parts, 1), o_ref, 2.0 ** -7), (S_whole, S_ref, 2.0 ** -18),
+                          (S, S_ref, 2.0 ** -18)):
+        assert np.linalg.norm(got.double().cpu().numpy() - ref) <= lim * np.linalg.norm(ref)
