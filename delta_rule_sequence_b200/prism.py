@@ -526,6 +526,11 @@ def _allocating_on(stream, device):
 _HERE = contextlib.nullcontext()
 
 
+def _new(like, shape) -> torch.Tensor:
+    """A new dense tensor of `like`'s type on its device (the cheapest of torch's ways to make one)."""
+    return torch.empty_like(like) if like.shape == shape and like.is_contiguous() else like.new_empty(shape)
+
+
 def _handed_out(stream, device, *tensors) -> None:
     """Results made on another stream than the current one: the current one, where the caller is going to use
     them, keeps their memory from being handed out again too early."""
@@ -610,9 +615,9 @@ def prism_decay_scan_fwd(q, k, v, decay, S0=None, lengths=None, *, o=None, S_fin
     _check_tensor("lengths", lengths, torch.int32, (B,), dev)
     with _allocating_on(stream, dev):
         if o is None:
-            o = torch.empty((B, T, H, dv), dtype=io, device=dev)
+            o = _new(q, (B, T, H, dv))
         if S_final is None and want_state:
-            S_final = torch.empty((B, H, dv, dk), dtype=f32, device=dev)
+            S_final = _new(decay if S0 is None else S0, (B, H, dv, dk))
         ws = _scratch("prism_decay_scan_fwd_workspace_size", shape, sizes, dev, workspace)
     _check_tensor("o", o, io, (B, T, H, dv), dev)
     _check_tensor("S_final", S_final, f32, (B, H, dv, dk), dev)
@@ -640,10 +645,8 @@ def prism_decay_scan_bwd(q, k, v, decay, S0=None, lengths=None, *, dO, dS_final=
     _check_tensor("dO", dO, io, (B, T, H, dv), dev)
     _check_tensor("dS_final", dS_final, f32, (B, H, dv, dk), dev)
     with _allocating_on(stream, dev):
-        out = {"dq": torch.empty((B, T, H, dk), dtype=io, device=dev),
-               "dk": torch.empty((B, T, Hkv, dk), dtype=io, device=dev),
-               "dv": torch.empty((B, T, Hkv, dv), dtype=io, device=dev),
-               "dS0": torch.empty((B, H, dv, dk), dtype=f32, device=dev) if want_dS0 else None}
+        out = {"dq": _new(q, q.shape), "dk": _new(k, k.shape), "dv": _new(v, v.shape),
+               "dS0": _new(decay if S0 is None else S0, (B, H, dv, dk)) if want_dS0 else None}
         ws = _scratch("prism_decay_scan_bwd_workspace_size", shape, sizes, dev, workspace)
     rc = _call(dev, lib.prism_decay_scan_bwd, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(S0),
                _ptr(lengths), _ptr(dO), _ptr(dS_final), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
@@ -665,7 +668,7 @@ def prism_decay_step(q, k, v, decay, S, *, o=None, stream=None):
     _check_tensor("S", S, torch.float32, (B, H, dv, dk), dev)
     if o is None:
         with _allocating_on(stream, dev):
-            o = torch.empty((B, T, H, dv), dtype=io, device=dev)
+            o = _new(q, (B, T, H, dv))
     _check_tensor("o", o, io, (B, T, H, dv), dev)
     rc = _call(dev, lib.prism_decay_step, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(S),
                _ptr(o), _stream(stream, dev))
@@ -714,7 +717,8 @@ def prism_group_norm_fwd(x, groups, weight=None, bias=None, gate=None, *, eps=1e
     with _allocating_on(stream, dev):
         if y is None:
             y = torch.empty_like(x)
-        mean, rstd = torch.empty((2, sizes[0], groups), dtype=torch.float32, device=dev).unbind(0)
+        mean = x.new_empty((sizes[0], groups), dtype=torch.float32)
+        rstd = torch.empty_like(mean)
         ws = _scratch("prism_group_norm_fwd_workspace_size", shape, sizes, dev, workspace)
     _check_tensor("y", y, io, x.shape, dev)
     rc = _call(dev, lib.prism_group_norm_fwd, ctypes.byref(shape), _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate),
