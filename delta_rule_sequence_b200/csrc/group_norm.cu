@@ -11,7 +11,9 @@
 //           side by side, a few lanes hold them in registers, one pass over the data.
 //   tiles   any S: a first kernel reduces tiles of positions, a second one merges the tiles' results
 //           and applies them (its reads of a tensor up to L2's size hit L2).  A thread keeps the same
-//           channels (one vector) for all of its positions, so any D works at full vector width.
+//           channels (one vector) for all of its positions, so any D works at full vector width.  (One kernel
+//           whose CTAs keep a sample in the shared memory of a cluster was measured: 53 us instead of 27 on
+//           8 samples of 4096 x 320, which takes clusters of 16.)
 // Means and variances are merged pairwise from centred sums (count, mean, sum of squares about the
 // mean): a mean far above the deviation costs no digits.
 
@@ -457,8 +459,6 @@ __global__ void __launch_bounds__(1024) norm_channel_sum_kernel(const float *par
 
 constexpr int kTileThreads = 256;
 constexpr int kTileCols = 256;  // vector columns of a block
-// positions that a thread requests at a time: for the statistics, for the outputs, for the gradients
-constexpr int kStatAhead = 8, kTileAhead = 4, kGradAhead = 2;
 
 struct Stat {
     float n, mean, m2;
@@ -499,6 +499,64 @@ struct Tile {
     __device__ long long at(const NormArgs &p, int s) const { return ((long long)n * p.S + s) * p.C + c0 + col * V; }
 };
 
+// A thread's vectors of the positions s0 + rl, s0 + rl + RL, ... of NT tensors (x, dy, gate; a null one is
+// skipped), AHEAD - 1 positions ahead of their use: asynchronous copies into shared memory, read back by the
+// same thread.  (Batches of plain loads, each waited for before the next, reached a third of the bandwidth.)
+// Vectors of less than 16 bytes are loaded when they are due.
+template <typename IO, int V, int NT>
+struct PosStream {
+    static constexpr bool RING = sizeof(Pack<IO, V>) == 16;
+    static constexpr int AHEAD = NT == 3 ? 5 : 8;  // (two blocks of 256 threads fit an SM)
+    const void *t[NT];
+    Pack<IO, V> *buf;  // shared, [AHEAD][NT][kTileThreads]
+    long long at, step;
+    int s, end, RL, slot;
+    __device__ PosStream(const NormArgs &p, const Tile<V> &tile, Pack<IO, V> *ring) : buf(ring) {
+        s = tile.s0 + tile.rl;
+        end = tile.live ? tile.s1 : tile.s0;
+        RL = tile.RL;
+        at = tile.at(p, s);
+        step = (long long)RL * p.C;
+        slot = 0;
+    }
+    __device__ __forceinline__ Pack<IO, V> *place(int sl, int k) const { return buf + (sl * NT + k) * kTileThreads + threadIdx.x; }
+    __device__ __forceinline__ void request(int ahead, int sl) {
+        if constexpr (RING) {
+            if (s + ahead * RL < end)
+#pragma unroll
+                for (int k = 0; k < NT; ++k)
+                    if (t[k]) {
+                        const uint32_t dst = (uint32_t)__cvta_generic_to_shared(place(sl, k));
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"((const IO *)t[k] + at + ahead * step)
+                                     : "memory");
+                    }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    }
+    __device__ __forceinline__ void start() {
+#pragma unroll
+        for (int k = 0; k + 1 < AHEAD; ++k) request(k, k);
+    }
+    __device__ __forceinline__ bool more() const { return s < end; }
+    // The current position's vectors; requests the one AHEAD - 1 further on.
+    __device__ __forceinline__ void get(Pack<IO, V> (&x)[NT]) {
+        if constexpr (RING) {
+            request(AHEAD - 1, (slot + AHEAD - 1) % AHEAD);
+            asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
+        }
+#pragma unroll
+        for (int k = 0; k < NT; ++k)
+            if (t[k]) x[k] = RING ? *place(slot, k) : load_pack<IO, V>(t[k], at);
+    }
+    __device__ __forceinline__ void next() {
+        s += RL;
+        at += step;
+        slot = (slot + 1) % AHEAD;
+    }
+};
+template <typename IO, int V, int NT>
+constexpr int kPosBytes = PosStream<IO, V, NT>::RING ? PosStream<IO, V, NT>::AHEAD * NT * kTileThreads * 16 : 0;
+
 __host__ __device__ inline int norm_pieces(int G, int blocks) { return G + blocks - 1; }
 
 template <typename IO, int V>
@@ -507,27 +565,23 @@ __global__ void __launch_bounds__(kTileThreads, 2) norm_tile_stats_kernel(NormAr
     dependent_wait();
     const Tile<V> t(p, blockIdx.x);
     const int D = p.C / p.G;
+    extern __shared__ __align__(16) uint8_t ring[];
+    PosStream<IO, V, 1> in(p, t, reinterpret_cast<Pack<IO, V> *>(ring));
+    in.t[0] = p.x;
     float mean[V] = {}, m2[V] = {};
     float cnt = 0.f;
-    if (t.live)
-        for (int s = t.s0 + t.rl; s < t.s1; s += kStatAhead * t.RL) {
-            Pack<IO, V> x[kStatAhead];
+    for (in.start(); in.more(); in.next()) {
+        Pack<IO, V> x[1];
+        in.get(x);
+        cnt += 1.f;
+        const float f = __fdividef(1.f, cnt);
 #pragma unroll
-            for (int u = 0; u < kStatAhead; ++u)
-                if (s + u * t.RL < t.s1) x[u] = load_pack<IO, V>(p.x, t.at(p, s + u * t.RL));
-#pragma unroll
-            for (int u = 0; u < kStatAhead; ++u) {
-                if (s + u * t.RL >= t.s1) break;
-                cnt += 1.f;
-                const float f = __fdividef(1.f, cnt);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float d = x[u].at(i) - mean[i];
-                    mean[i] = fmaf(d, f, mean[i]);
-                    m2[i] = fmaf(d, x[u].at(i) - mean[i], m2[i]);
-                }
-            }
+        for (int i = 0; i < V; ++i) {
+            const float d = x[0].at(i) - mean[i];
+            mean[i] = fmaf(d, f, mean[i]);
+            m2[i] = fmaf(d, x[0].at(i) - mean[i], m2[i]);
         }
+    }
     const int width = t.c1 - t.c0;
     if (t.live)
 #pragma unroll
@@ -595,6 +649,11 @@ __global__ void __launch_bounds__(kTileThreads, 2) norm_tile_apply_kernel(NormAr
     __shared__ float sh_mean[kTileCols * V], sh_rstd[kTileCols * V];
     const Tile<V> t(p, blockIdx.x);
     const int D = p.C / p.G, g0 = t.first_group(D);
+    extern __shared__ __align__(16) uint8_t ring[];
+    PosStream<IO, V, 2> in(p, t, reinterpret_cast<Pack<IO, V> *>(ring));
+    in.t[0] = p.x;
+    in.t[1] = mode_gate<MODE>(p) ? p.gate : nullptr;
+    in.start();
     dependent_wait();
     for (int g = g0 + kGroupsAtOnce * (threadIdx.x >> 5); g <= t.last_group(D); g += kGroupsAtOnce * (kTileThreads / 32)) {
         Stat st[kGroupsAtOnce] = {};
@@ -625,22 +684,12 @@ __global__ void __launch_bounds__(kTileThreads, 2) norm_tile_apply_kernel(NormAr
         w[i] = p.weight ? p.weight[c] : 1.f;
         b[i] = p.bias ? p.bias[c] : 0.f;
     }
-    for (int s = t.s0 + t.rl; s < t.s1; s += kTileAhead * t.RL) {
-        Pack<IO, V> x[kTileAhead], gt[kTileAhead];
+    for (; in.more(); in.next()) {
+        Pack<IO, V> x[2], y;
+        in.get(x);
 #pragma unroll
-        for (int u = 0; u < kTileAhead; ++u)
-            if (s + u * t.RL < t.s1) {
-                x[u] = load_pack<IO, V>(p.x, t.at(p, s + u * t.RL));
-                if (mode_gate<MODE>(p)) gt[u] = load_pack<IO, V>(p.gate, t.at(p, s + u * t.RL));
-            }
-#pragma unroll
-        for (int u = 0; u < kTileAhead; ++u) {
-            if (s + u * t.RL >= t.s1) break;
-            Pack<IO, V> y;
-#pragma unroll
-            for (int i = 0; i < V; ++i) st_io(y.v, i, y_of<IO, MODE>(p, fmaf((x[u].at(i) - mean[i]) * rstd[i], w[i], b[i]), gt[u].at(i)));
-            store_pack<IO, V>(p.y, t.at(p, s + u * t.RL), y);
-        }
+        for (int i = 0; i < V; ++i) st_io(y.v, i, y_of<IO, MODE>(p, fmaf((x[0].at(i) - mean[i]) * rstd[i], w[i], b[i]), x[1].at(i)));
+        store_pack<IO, V>(p.y, in.at, y);
     }
 }
 
@@ -651,12 +700,18 @@ template <typename IO, int V, int MODE>
 __global__ void __launch_bounds__(kTileThreads, 2) norm_tile_grad_sums_kernel(NormArgs p) {
     __shared__ float sh1[kTileThreads * V], sh2[kTileThreads * V];
     __shared__ float tot1[kTileCols * V], tot2[kTileCols * V];
+    extern __shared__ __align__(16) uint8_t ring[];
     const int D = p.C / p.G;
     dependent_wait();
     for (int i = threadIdx.x; i < kTileCols * V; i += kTileThreads) tot1[i] = tot2[i] = 0.f;
     for (int unit = blockIdx.x; unit < p.N * p.tiles; unit += gridDim.x) {
         const Tile<V> t(p, unit);
         const int width = t.c1 - t.c0;
+        PosStream<IO, V, 3> in(p, t, reinterpret_cast<Pack<IO, V> *>(ring));
+        in.t[0] = p.x;
+        in.t[1] = p.dy;
+        in.t[2] = mode_gate<MODE>(p) ? p.gate : nullptr;
+        in.start();
         __syncthreads();
         if (t.live) {
             float mean[V], rstd[V], w[V], b[V], sz[V] = {}, szx[V] = {};
@@ -668,27 +723,16 @@ __global__ void __launch_bounds__(kTileThreads, 2) norm_tile_grad_sums_kernel(No
                 w[i] = p.weight ? p.weight[c] : 1.f;
                 b[i] = p.bias ? p.bias[c] : 0.f;
             }
-            for (int s = t.s0 + t.rl; s < t.s1; s += kGradAhead * t.RL) {
-                Pack<IO, V> x[kGradAhead], dy[kGradAhead], gt[kGradAhead];
+            for (; in.more(); in.next()) {
+                Pack<IO, V> x[3];
+                in.get(x);
 #pragma unroll
-                for (int u = 0; u < kGradAhead; ++u)
-                    if (s + u * t.RL < t.s1) {
-                        const long long at = t.at(p, s + u * t.RL);
-                        x[u] = load_pack<IO, V>(p.x, at);
-                        dy[u] = load_pack<IO, V>(p.dy, at);
-                        if (mode_gate<MODE>(p)) gt[u] = load_pack<IO, V>(p.gate, at);
-                    }
-#pragma unroll
-                for (int u = 0; u < kGradAhead; ++u) {
-                    if (s + u * t.RL >= t.s1) break;
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float xh = (x[u].at(i) - mean[i]) * rstd[i];
-                        float dg;
-                        const float dz = dz_of<IO, MODE>(p, fmaf(xh, w[i], b[i]), dy[u].at(i), gt[u].at(i), dg);
-                        sz[i] += dz;
-                        szx[i] = fmaf(dz, xh, szx[i]);
-                    }
+                for (int i = 0; i < V; ++i) {
+                    const float xh = (x[0].at(i) - mean[i]) * rstd[i];
+                    float dg;
+                    const float dz = dz_of<IO, MODE>(p, fmaf(xh, w[i], b[i]), x[1].at(i), x[2].at(i), dg);
+                    sz[i] += dz;
+                    szx[i] = fmaf(dz, xh, szx[i]);
                 }
             }
 #pragma unroll
@@ -742,6 +786,12 @@ __global__ void __launch_bounds__(kTileThreads, 2) norm_tile_grad_apply_kernel(N
     __shared__ float sh1[kTileCols * V], sh2[kTileCols * V];
     const Tile<V> t(p, blockIdx.x);
     const int D = p.C / p.G, g0 = t.first_group(D), lane = threadIdx.x & 31;
+    extern __shared__ __align__(16) uint8_t ring[];
+    PosStream<IO, V, 3> in(p, t, reinterpret_cast<Pack<IO, V> *>(ring));
+    in.t[0] = p.x;
+    in.t[1] = p.dy;
+    in.t[2] = mode_gate<MODE>(p) ? p.gate : nullptr;
+    in.start();
     dependent_wait();
     const float inv = 1.f / ((float)D * (float)p.S);
     for (int g = g0 + kGroupsAtOnce * (threadIdx.x >> 5); g <= t.last_group(D); g += kGroupsAtOnce * (kTileThreads / 32)) {
@@ -772,32 +822,19 @@ __global__ void __launch_bounds__(kTileThreads, 2) norm_tile_grad_apply_kernel(N
         s1[i] = sh1[g - g0];
         s2[i] = sh2[g - g0];
     }
-    for (int s = t.s0 + t.rl; s < t.s1; s += kGradAhead * t.RL) {
-        Pack<IO, V> x[kGradAhead], dy[kGradAhead], gt[kGradAhead];
+    for (; in.more(); in.next()) {
+        Pack<IO, V> x[3], dgv, dxv;
+        in.get(x);
 #pragma unroll
-        for (int u = 0; u < kGradAhead; ++u)
-            if (s + u * t.RL < t.s1) {
-                const long long at = t.at(p, s + u * t.RL);
-                x[u] = load_pack<IO, V>(p.x, at);
-                dy[u] = load_pack<IO, V>(p.dy, at);
-                if (mode_gate<MODE>(p)) gt[u] = load_pack<IO, V>(p.gate, at);
-            }
-#pragma unroll
-        for (int u = 0; u < kGradAhead; ++u) {
-            if (s + u * t.RL >= t.s1) break;
-            const long long at = t.at(p, s + u * t.RL);
-            Pack<IO, V> dgv, dxv;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float xh = (x[u].at(i) - mean[i]) * rstd[i];
-                float dg;
-                const float dz = dz_of<IO, MODE>(p, fmaf(xh, w[i], b[i]), dy[u].at(i), gt[u].at(i), dg);
-                st_io(dxv.v, i, rstd[i] * (fmaf(dz, w[i], -s1[i]) - xh * s2[i]));
-                st_io(dgv.v, i, dg);
-            }
-            store_pack<IO, V>(p.dx, at, dxv);
-            if (mode_gate<MODE>(p)) store_pack<IO, V>(p.dgate, at, dgv);
+        for (int i = 0; i < V; ++i) {
+            const float xh = (x[0].at(i) - mean[i]) * rstd[i];
+            float dg;
+            const float dz = dz_of<IO, MODE>(p, fmaf(xh, w[i], b[i]), x[1].at(i), x[2].at(i), dg);
+            st_io(dxv.v, i, rstd[i] * (fmaf(dz, w[i], -s1[i]) - xh * s2[i]));
+            st_io(dgv.v, i, dg);
         }
+        store_pack<IO, V>(p.dx, in.at, dxv);
+        if (mode_gate<MODE>(p)) store_pack<IO, V>(p.dgate, in.at, dgv);
     }
 }
 
@@ -865,6 +902,16 @@ void with_mode(const NormArgs &a, F f) {
     }
 }
 
+// Launch of a tiles kernel with its stream's shared memory.
+template <int BYTES, typename K>
+cudaError_t launch_tiles(K kern, dim3 grid, const NormArgs &a, cudaStream_t s, bool dependent) {
+    if (BYTES > 0) {
+        const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+        if (err != cudaSuccess) return err;
+    }
+    return dependent_launch(kern, grid, kTileThreads, BYTES, s, dependent, a);
+}
+
 // f(lanes) with the plan's lanes of a group as a compile-time number.
 template <typename F>
 void with_lanes(int LG, F f) {
@@ -879,8 +926,8 @@ void with_lanes(int LG, F f) {
 template <typename IO>
 cudaError_t launch_fwd(const NormArgs &a, const NormPlan &pl, cudaStream_t s) {
     constexpr int F = 16 / sizeof(IO);
-    launch_probe_mark(s);
     if (pl.rows) {
+        launch_probe_mark(s);
         with_lanes(pl.LG, [&](auto l) {
             if (pl.V == 1) norm_rows_fwd_kernel<IO, 1, kRowVecs, l.value, kRuntime><<<pl.blocks, kRowThreads, 0, s>>>(a, pl.row_lanes);
             else if (pl.K == 1)
@@ -891,11 +938,11 @@ cudaError_t launch_fwd(const NormArgs &a, const NormPlan &pl, cudaStream_t s) {
         return cudaGetLastError();
     }
     const dim3 grid(a.N * a.tiles, pl.col_blocks);
-    (pl.V == 1 ? norm_tile_stats_kernel<IO, 1> : norm_tile_stats_kernel<IO, F>)<<<grid, kTileThreads, 0, s>>>(a);
-    cudaError_t err = cudaGetLastError();
+    cudaError_t err = pl.V == 1 ? launch_tiles<0>(norm_tile_stats_kernel<IO, 1>, grid, a, s, false)
+                                : launch_tiles<kPosBytes<IO, F, 1>>(norm_tile_stats_kernel<IO, F>, grid, a, s, false);
     if (err != cudaSuccess) return err;
-    if (pl.V == 1) err = dependent_launch(norm_tile_apply_kernel<IO, 1, kRuntime>, grid, kTileThreads, 0, s, true, a);
-    else with_mode(a, [&](auto m) { err = dependent_launch(norm_tile_apply_kernel<IO, F, m.value>, grid, kTileThreads, 0, s, true, a); });
+    if (pl.V == 1) err = launch_tiles<0>(norm_tile_apply_kernel<IO, 1, kRuntime>, grid, a, s, true);
+    else with_mode(a, [&](auto m) { err = launch_tiles<kPosBytes<IO, F, 2>>(norm_tile_apply_kernel<IO, F, m.value>, grid, a, s, true); });
     return err;
 }
 
@@ -903,8 +950,8 @@ template <typename IO>
 cudaError_t launch_bwd(const NormArgs &a, const NormPlan &pl, float *dweight, float *dbias, cudaStream_t s) {
     constexpr int F = 16 / sizeof(IO);
     cudaError_t err = cudaSuccess;
-    launch_probe_mark(s);
     if (pl.rows) {
+        launch_probe_mark(s);
         with_lanes(pl.LG, [&](auto l) {
             if (pl.V == 1) norm_rows_bwd_kernel<IO, 1, kRowVecs, l.value, kRuntime><<<pl.blocks, kRowThreads, 0, s>>>(a, pl.row_lanes);
             else if (pl.K == 1)
@@ -914,11 +961,12 @@ cudaError_t launch_bwd(const NormArgs &a, const NormPlan &pl, float *dweight, fl
         });
     } else {
         const dim3 grid(a.N * a.tiles, pl.col_blocks);
-        if (pl.V == 1) norm_tile_grad_sums_kernel<IO, 1, kRuntime><<<dim3(a.parts, pl.col_blocks), kTileThreads, 0, s>>>(a);
-        else with_mode(a, [&](auto m) { norm_tile_grad_sums_kernel<IO, F, m.value><<<dim3(a.parts, pl.col_blocks), kTileThreads, 0, s>>>(a); });
-        if ((err = cudaGetLastError()) != cudaSuccess) return err;
-        if (pl.V == 1) err = dependent_launch(norm_tile_grad_apply_kernel<IO, 1, kRuntime>, grid, kTileThreads, 0, s, true, a);
-        else with_mode(a, [&](auto m) { err = dependent_launch(norm_tile_grad_apply_kernel<IO, F, m.value>, grid, kTileThreads, 0, s, true, a); });
+        const dim3 some(a.parts, pl.col_blocks);
+        if (pl.V == 1) err = launch_tiles<0>(norm_tile_grad_sums_kernel<IO, 1, kRuntime>, some, a, s, false);
+        else with_mode(a, [&](auto m) { err = launch_tiles<kPosBytes<IO, F, 3>>(norm_tile_grad_sums_kernel<IO, F, m.value>, some, a, s, false); });
+        if (err != cudaSuccess) return err;
+        if (pl.V == 1) err = launch_tiles<0>(norm_tile_grad_apply_kernel<IO, 1, kRuntime>, grid, a, s, true);
+        else with_mode(a, [&](auto m) { err = launch_tiles<kPosBytes<IO, F, 3>>(norm_tile_grad_apply_kernel<IO, F, m.value>, grid, a, s, true); });
     }
     if (err == cudaSuccess) err = cudaGetLastError();
     if (err == cudaSuccess && (dweight || dbias))
