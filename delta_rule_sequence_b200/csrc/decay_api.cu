@@ -28,13 +28,14 @@ bool make_operand(const prism_decay_shape &s, const void *p, const long long (&s
     const bool is_dense = st[0] == 0 && st[1] == 0 && st[2] == 0;
     const long long unit = 16 / (long long)io_bytes(s.io);
     long long r[3], last = d;
+    const bool empty = s.B == 0 || s.T == 0 || heads == 0;
     for (int i = 0; i < 3; ++i) {
         r[i] = is_dense || n[i] <= 1 ? dense[i] : st[i];
-        if (n[i] > 1 && s.T > 0 && (r[i] <= 0 || r[i] % unit || r[i] >= 1LL << 36)) return false;
+        if (n[i] > 1 && !empty && (r[i] <= 0 || r[i] % unit || r[i] >= 1LL << 36)) return false;
         if (n[i] > 1) last += (n[i] - 1) * r[i];
     }
     out->t = DecayTensor{p, r[0], r[1], r[2], heads > 0 ? s.H / heads : 1};
-    out->extent = (size_t)last * io_bytes(s.io);
+    out->extent = empty ? 0 : (size_t)last * io_bytes(s.io);
     return true;
 }
 
@@ -200,7 +201,7 @@ prism_status prism_decay_scan_fwd(const prism_decay_shape *shape, const void *q,
     const ByteRange outs[] = {{o, (size_t)s.B * s.T * s.H * s.dv * io_bytes(s.io)}, {S_final, state}, {workspace, need}};
     const ByteRange ins[] = {{q, c.q.extent}, {k, c.k.extent}, {v, c.v.extent}, {decay, (size_t)s.H * 4},
                          {lengths, (size_t)s.B * 4}, {S_final == S0 ? nullptr : S0, state}};
-    if (c.work && outputs_alias(outs, 3, ins, 6)) return PRISM_ERR_INVALID_ARG;
+    if (outputs_alias(outs, 3, ins, 6)) return PRISM_ERR_INVALID_ARG;
     if (s.B == 0 || s.H == 0) return PRISM_OK;
     Runner r{s, plan_of(s, 1, lengths != nullptr), decay, lengths, (cudaStream_t)stream};
     float *F = (float *)workspace;
@@ -248,7 +249,7 @@ prism_status prism_decay_scan_bwd(const prism_decay_shape *shape, const void *q,
                           {workspace, need}};
     const ByteRange ins[] = {{q, c.q.extent}, {k, c.k.extent}, {v, c.v.extent}, {decay, (size_t)s.H * 4}, {lengths, (size_t)s.B * 4},
                          {S0, state}, {dO, rows * s.H * s.dv}, {dS_final, state}};
-    if (c.work && outputs_alias(outs, 5, ins, 8)) return PRISM_ERR_INVALID_ARG;
+    if (outputs_alias(outs, 5, ins, 8)) return PRISM_ERR_INVALID_ARG;
     if (s.B == 0 || s.H == 0) return PRISM_OK;
     Runner r{s, plan_of(s, 3, lengths != nullptr), decay, lengths, (cudaStream_t)stream};
     if (s.T == 0) {

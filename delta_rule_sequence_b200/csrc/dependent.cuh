@@ -30,7 +30,9 @@ cudaError_t dependent_launch(void (*kern)(P...), dim3 grid, int threads, size_t 
     cfg.attrs = &attr;
     cfg.numAttrs = dependent ? 1 : 0;
     launch_probe_mark(s);
-    return cudaLaunchKernelEx(&cfg, kern, args...);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, args...);
+    if (err != cudaSuccess) cudaGetLastError();  // reported here, not by the caller's next check
+    return err;
 }
 
 }  // namespace prism

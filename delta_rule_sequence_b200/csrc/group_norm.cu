@@ -887,7 +887,8 @@ prism_status check_shape(const prism_norm_shape *s) {
     if (s->io != PRISM_BF16 && s->io != PRISM_F32) return PRISM_ERR_INVALID_ARG;
     if (s->act != PRISM_ACT_NONE && s->act != PRISM_ACT_SILU && s->act != PRISM_ACT_GELU) return PRISM_ERR_INVALID_ARG;
     if (!(s->eps >= 0.f)) return PRISM_ERR_INVALID_ARG;
-    if (s->C > (1 << 20) || (long long)s->N * s->G > 0x7fffffffLL || s->N > (1 << 24)) return PRISM_ERR_UNSUPPORTED;
+    if (s->C > (1 << 20) || (long long)s->N * s->G > 0x7fffffffLL || s->N > (1 << 24) || s->S > (1 << 30)) return PRISM_ERR_UNSUPPORTED;
+    if ((long long)s->N * s->S > (1LL << 40) / s->C) return PRISM_ERR_UNSUPPORTED;  // (sizes in bytes stay far below 2^63)
     return PRISM_OK;
 }
 

@@ -566,13 +566,21 @@ def _view_strides(name, x, dtype, shape, device):
 _DENSE = (0, 0, 0)  # prism_decay_shape: the dense layout
 
 
+def _check_ints(sizes):
+    """The shape structures hold C ints, which ctypes would cut larger values to."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise ValueError(f"sizes must be below 2^31, got {sizes}")
+
+
 @functools.lru_cache(maxsize=4096)
 def _decay_shape(sizes, *strides):
+    _check_ints(sizes)
     return PrismDecayShape(*sizes, *strides)  # read only by the library
 
 
 @functools.lru_cache(maxsize=4096)
 def _norm_shape(sizes):
+    _check_ints(sizes[:6])
     return PrismNormShape(*sizes)
 
 
@@ -695,8 +703,6 @@ def _norm_inputs(x, groups, weight, bias, gate, eps, activation):
         S *= n
     if groups < 1 or C < 1 or C % groups:
         raise ValueError(f"{groups} groups do not divide {C} channels")
-    if S > 0x7FFFFFFF:
-        raise ValueError(f"x has {S} positions, the library takes up to 2^31 - 1")
     _check_tensor("x", x, io, x.shape, dev)
     _check_tensor("weight", weight, torch.float32, (C,), dev)
     _check_tensor("bias", bias, torch.float32, (C,), dev)

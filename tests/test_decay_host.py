@@ -92,6 +92,7 @@ def test_decay_scan_refuses_overlap(lib):
     assert bwd(lib, s, dq=ptr(1)) == INVALID
     assert bwd(lib, s, dv=ptr(10, 32)) == INVALID
     assert bwd(lib, s, dS0=ptr(8)) == INVALID
+    assert fwd(lib, shape(T=0), S_final=ptr(5, 16)) == INVALID  # without tokens, too
     # a view's extent counts, not its dense size: batch stride 1 MB
     wide = shape(q=(MB // 2, 256, 64))
     assert fwd(lib, wide, o=ptr(1, MB + 1024)) == INVALID
@@ -143,6 +144,7 @@ def nbwd(lib, s, ws_bytes=1 << 30, **kw):
     (dict(G=5), INVALID), (dict(G=0), INVALID), (dict(C=0), INVALID), (dict(N=-1), INVALID), (dict(S=-1), INVALID),
     (dict(io=3), INVALID), (dict(act=3), INVALID), (dict(act=-1), INVALID), (dict(eps=-1.0), INVALID),
     (dict(eps=float("nan")), INVALID), (dict(C=1 << 21), UNSUPPORTED), (dict(N=1 << 25), UNSUPPORTED),
+    (dict(S=(1 << 30) + 1), UNSUPPORTED), (dict(N=1 << 24, S=1 << 30, C=1 << 20, G=1), UNSUPPORTED),
 ])
 def test_group_norm_refuses_shapes(lib, kw, want):
     assert nfwd(lib, nshape(**kw)) == want
@@ -180,3 +182,11 @@ def test_wrappers_refuse_cpu_tensors():
         P.prism_group_norm_fwd(q, 2)
     with pytest.raises(TypeError):
         P.prism_group_norm_bwd(q, 2, a, a, dy=q)
+
+
+def test_wrappers_refuse_sizes_beyond_c_ints():
+    """2^32 + 1 would arrive in the library as 1."""
+    with pytest.raises(ValueError):
+        P._norm_shape(((1 << 32) + 1, 1, 8, 2, P.PRISM_BF16, 0, 1e-5))
+    with pytest.raises(ValueError):
+        P._decay_shape((1, 1, (1 << 32) + 1, 1, 32, 32, P.PRISM_BF16), P._DENSE, P._DENSE, P._DENSE)
