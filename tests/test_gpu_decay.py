@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from oracle.decay_scan import decay_scan_ref
+from oracle.decay_scan import decay_scan_grad_ref, decay_scan_ref
 from tests.decay_checks import check, check_bwd, check_fwd, make
 
 pytestmark = pytest.mark.gpu
@@ -332,3 +332,73 @@ def test_a_stalled_pipeline_gives_up():
     assert P.prism_query_device_status(None) == P.PRISM_OK
     got = fwd(x)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+def test_a_workspace_with_any_contents(io):
+    x = make(35, 2, 700, 4, 2, 64, 64, io, ragged=True)
+    dO, dS = grads_of(36, x)
+    want, wantg = fwd(x), bwd(x, dO, dS)
+    ws = torch.full((64 << 20,), 255, dtype=torch.uint8, device="cuda")  # every float a NaN
+    got = fwd(x, workspace=ws)
+    ws.fill_(255)
+    gotg = bwd(x, dO, dS, workspace=ws)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert all(torch.equal(gotg[n], wantg[n]) for n in wantg)
+    with pytest.raises(prism().PrismError):
+        fwd(x, workspace=ws[:256])
+
+
+def test_first_calls_of_a_process_under_capture():
+    """No warm-up before the capture: what a call looks up on first use is allowed there."""
+    import os
+    import subprocess
+    import sys
+
+    code = """
+import torch
+from delta_rule_sequence_b200 import prism as P
+q, k, v = (torch.randn(1, 200, 2, 64, device="cuda").bfloat16() for _ in range(3))
+a = torch.full((2,), 0.9, device="cuda")
+S = torch.zeros(1, 2, 64, 64, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    o, _ = P.prism_decay_scan_fwd(q, k, v, a)
+    gr = P.prism_decay_scan_bwd(q, k, v, a, dO=o)
+    P.prism_decay_step(q[:, :1], k[:, :1], v[:, :1], a, S)
+    y, m, r = P.prism_group_norm_fwd(o.view(200, 128), 2, activation="silu")
+    n = P.prism_group_norm_bwd(o.view(1, 200, 128), 2, m[:1], r[:1], dy=o.view(1, 200, 128))
+g.replay()
+torch.cuda.synchronize()
+want, _ = P.prism_decay_scan_fwd(q, k, v, a)
+torch.cuda.synchronize()
+assert torch.equal(o, want) and torch.isfinite(gr["dq"].float()).all()
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_offsets_beyond_31_bits():
+    """2^20 tokens of 17 x 128: the operands' last elements lie behind 2^31 (and the fp32 partial gradients of the
+    shared head behind 2^33 bytes).  With a decay of 1/2 a token's reach ends after 512 (2^-512 times its mass), so
+    the last 1024 tokens alone give the last 512 tokens' results."""
+    T, H, d = 1 << 20, 17, 128
+    g = torch.Generator(device="cuda").manual_seed(37)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=BF)  # noqa: E731
+    x = {"q": r(1, T, H, d), "k": r(1, T, 1, d) * d ** -0.5, "v": r(1, T, 1, d), "decay": torch.full((H,), 0.5, device="cuda"),
+         "S0": None, "lengths": None}
+    dO = r(1, T, H, d)
+    o, S = fwd(x)
+    got = bwd(x, dO)
+    tail = {n: t[:, -1024:].contiguous() if n in "qkv" else t for n, t in x.items()}
+    mass = {n: t.float().abs() if n in "qkv" else t for n, t in tail.items()}
+    ref, m = decay_scan_ref(**tail), decay_scan_ref(**mass)
+    check("o", o[:, -512:], ref[0][:, -512:], m[0][:, -512:], True)
+    check("S_final", S, ref[1], m[1], False)
+    args = {"do": dO[:, -1024:], "dS_final": None}
+    ref = decay_scan_grad_ref(**tail, **args)
+    m = decay_scan_grad_ref(**mass, do=args["do"].float().abs(), dS_final=None)
+    for n in ("dq", "dk", "dv"):
+        check(n, got[n][:, -512:], ref[n][:, -512:], m[n][:, -512:], True)

@@ -63,10 +63,9 @@ def run_and_check(x, G, activation, eps=1e-5, flat=False):
     near("dx", got["dx"], g["dx"], 4 * xh ** 2 * dy.max() * np.repeat(r[:, None, :], C // G, axis=2).reshape(N, 1, C), io)
     if x["gate"] is not None:
         near("dgate", got["dgate"], g["dgate"], xh * (1 + dy), io)
-    if x["weight"] is not None:
-        terms = (dy * gate * xh).sum((0, 1))
-        near("dweight", got["dweight"], g["dweight"], terms, F32)
-        near("dbias", got["dbias"], g["dbias"], terms, F32)
+    for n in ("dweight", "dbias"):
+        if n in got:
+            near(n, got[n], g[n], (dy * gate * xh).sum((0, 1)), F32)
     return y, mean, rstd, got
 
 
@@ -93,6 +92,14 @@ def test_shapes(io, N, S, C, G):
 @pytest.mark.parametrize("S", [1, 64])
 def test_no_weights(io, S):
     run_and_check(make(3, 6, S, 64, io, False, False), 4, "gelu")
+
+
+@pytest.mark.parametrize("S", [1, 64])
+@pytest.mark.parametrize("only", ["weight", "bias"])
+def test_weight_or_bias_alone(S, only):
+    x = make(11, 5, S, 96, BF, True, True)
+    x["bias" if only == "weight" else "weight"] = None
+    run_and_check(x, 6, "silu")
 
 
 @pytest.mark.parametrize("S", [1, 300])
@@ -200,3 +207,58 @@ def test_wrappers_refuse():
         P.prism_group_norm_fwd(x["x"], 4, y=x["x"])
     with pytest.raises(P.PrismError):
         P.prism_group_norm_fwd(x["x"], 4, eps=-1.0)
+
+
+def test_a_larger_workspace_and_given_outputs():
+    P = prism()
+    for S in (1, 70):
+        x = make(12, 4, S, 64, BF, False, True)
+        want, m, r = P.prism_group_norm_fwd(x["x"], 4, x["weight"], x["bias"])
+        ws = torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")  # any contents
+        y = torch.full_like(x["x"], float("nan"))
+        got, m2, r2 = P.prism_group_norm_fwd(x["x"], 4, x["weight"], x["bias"], y=y, workspace=ws)
+        g = P.prism_group_norm_bwd(x["x"], 4, m, r, x["weight"], x["bias"], dy=x["dy"])
+        ws.fill_(255)
+        g2 = P.prism_group_norm_bwd(x["x"], 4, m, r, x["weight"], x["bias"], dy=x["dy"], workspace=ws)
+        torch.cuda.synchronize()
+        assert got is y and torch.equal(y, want) and torch.equal(m, m2) and torch.equal(r, r2)
+        assert all(torch.equal(g[n], g2[n]) for n in g)
+
+
+def test_rows_behind_31_bits():
+    """Every row on its own: the last rows of 2.3e9 elements have the bits that they have alone."""
+    P = prism()
+    N, C, G = (1 << 20) + 5, 17 * 128, 17
+    g = torch.Generator(device="cuda").manual_seed(13)
+    x, dy = (torch.randn(N, C, generator=g, device="cuda", dtype=BF) for _ in range(2))
+    y, mean, rstd = P.prism_group_norm_fwd(x, G, gate=dy, activation="silu")
+    got = P.prism_group_norm_bwd(x, G, mean, rstd, gate=x, dy=dy, activation="silu")
+    y1, m1, r1 = P.prism_group_norm_fwd(x[-999:], G, gate=dy[-999:], activation="silu")
+    got1 = P.prism_group_norm_bwd(x[-999:], G, m1, r1, gate=x[-999:], dy=dy[-999:], activation="silu")
+    assert torch.equal(y[-999:], y1) and torch.equal(mean[-999:], m1) and torch.equal(rstd[-999:], r1)
+    assert all(torch.equal(got[n][-999:], got1[n]) for n in got1)
+
+
+def test_positions_behind_31_bits():
+    """The last of three samples of 2^20 x 768 against 64 bits."""
+    P = prism()
+    N, S, C, G = 3, 1 << 20, 768, 8
+    g = torch.Generator(device="cuda").manual_seed(14)
+    x, dy = (torch.randn(N, S, C, generator=g, device="cuda", dtype=BF) for _ in range(2))
+    y, mean, rstd = P.prism_group_norm_fwd(x, G)
+    dx = P.prism_group_norm_bwd(x, G, mean, rstd, dy=dy)["dx"]
+    xd = x[2].double().view(S, G, C // G)
+    m = xd.mean((0, 2))
+    r = (xd.var((0, 2), unbiased=False) + 1e-5).rsqrt()
+    big = xd.abs().max()
+    assert ((mean[2] - m).abs() <= 2.0 ** -21 * (1 + big)).all()
+    assert ((rstd[2] - r).abs() <= 2.0 ** -20 * r * (1 + big * r)).all()
+    xh = (xd - m[:, None]) * r[:, None]
+    del xd
+    cond = float(1 + big * r.max())
+    tol = 2.0 ** -18 * cond * 2
+    assert ((y[2].view(S, G, -1) - xh).abs() <= tol + 2.0 ** -8 * xh.abs()).all()
+    d = dy[2].double().view(S, G, C // G)
+    ref = (d - d.mean((0, 2))[:, None] - xh * (d * xh).mean((0, 2))[:, None]) * r[:, None]
+    tol = 2.0 ** -18 * 4 * (2 * cond) ** 2 * float(d.abs().max() * r.max())
+    assert ((dx[2].view(S, G, -1) - ref).abs() <= tol + 2.0 ** -8 * ref.abs()).all()
