@@ -12,7 +12,7 @@
 //   tiles   any S: a first kernel reduces tiles of positions, a second one merges the tiles' results
 //           and applies them (its reads of a tensor up to L2's size hit L2).  A thread keeps the same
 //           channels (one vector) for all of its positions, so any D works at full vector width.  (One kernel
-//           whose CTAs keep a sample in the shared memory of a cluster was measured: 53 us instead of 27 on
+//           whose CTAs keep a sample in the shared memory of a cluster was measured: 53 us against 27 on
 //           8 samples of 4096 x 320, which takes clusters of 16.)
 // Means and variances are merged pairwise from centred sums (count, mean, sum of squares about the
 // mean): a mean far above the deviation costs no digits.
@@ -35,9 +35,10 @@ struct NormArgs {
     const float *weight, *bias;
     float *mean, *rstd;      // outputs of the forward pass (may be null), inputs of the backward one
     void *y, *dx, *dgate;
-    float *stat_parts;       // tiles form: [N][tiles][pieces][2]
+    float *stat_parts;       // tiles form: [N][pieces][tiles][2]
     float *chan_parts;       // backward: [parts][2][C] sums of dz and dz xh
     int tiles, parts;
+    int tile_len, tile_more;  // tiles form: positions of a tile, and how many first tiles have one more
 };
 
 // ---- activations -------------------------------------------------------------------------------
@@ -93,6 +94,11 @@ using Unit = std::conditional_t<V == 1, float, F2>;
 template <int V>
 constexpr int kUnits = V == 1 ? 1 : V / 2;
 
+template <int V>
+__device__ __forceinline__ Unit<V> unit_of(const float (&x)[V], int u) {
+    if constexpr (V == 1) return x[0];
+    else return pack2(x[2 * u], x[2 * u + 1]);
+}
 template <typename U>
 __device__ __forceinline__ U both(float x) {
     if constexpr (sizeof(U) == 4) return x;
@@ -460,19 +466,6 @@ __global__ void __launch_bounds__(1024) norm_channel_sum_kernel(const float *par
 constexpr int kTileThreads = 256;
 constexpr int kTileCols = 256;  // vector columns of a block
 
-struct Stat {
-    float n, mean, m2;
-};
-__device__ __forceinline__ Stat merge(const Stat &a, const Stat &b) {
-    const float n = a.n + b.n;
-    if (n == 0.f) return a;
-    const float f = __fdividef(b.n, n), d = b.mean - a.mean;
-    return Stat{n, fmaf(d, f, a.mean), a.m2 + b.m2 + d * d * a.n * f};
-}
-__device__ __forceinline__ Stat shfl(const Stat &a, int o) {
-    return Stat{__shfl_xor_sync(0xffffffffu, a.n, o), __shfl_xor_sync(0xffffffffu, a.mean, o), __shfl_xor_sync(0xffffffffu, a.m2, o)};
-}
-
 // Geometry of a block: channels [c0, c1) (whole vectors), positions [s0, s1) of sample n; thread
 // (col, rl) owns V channels and every RL-th position.
 template <int V>
@@ -490,9 +483,10 @@ struct Tile {
         col = threadIdx.x % cols;
         rl = threadIdx.x / cols;
         live = rl < RL;
-        s0 = (int)((long long)p.S * tile / p.tiles);
-        s1 = (int)((long long)p.S * (tile + 1) / p.tiles);
+        s0 = tile * p.tile_len + min(tile, p.tile_more);
+        s1 = s0 + positions(p, tile);
     }
+    __device__ __forceinline__ static int positions(const NormArgs &p, int tile) { return p.tile_len + (tile < p.tile_more); }
     // A group cut by a block's edge leaves one piece in each block: piece g + cb is group g's in block cb.
     __device__ int first_group(int D) const { return c0 / D; }
     __device__ int last_group(int D) const { return (c1 - 1) / D; }
@@ -558,6 +552,49 @@ template <typename IO, int V, int NT>
 constexpr int kPosBytes = PosStream<IO, V, NT>::RING ? PosStream<IO, V, NT>::AHEAD * NT * kTileThreads * 16 : 0;
 
 __host__ __device__ inline int norm_pieces(int G, int blocks) { return G + blocks - 1; }
+// Where the pair of a group's piece in column block cb is, among stat_parts' pairs.
+__device__ __forceinline__ long long piece_at(const NormArgs &p, int n, int tile, int g, int cb, int blocks) {
+    return ((long long)n * norm_pieces(p.G, blocks) + g + cb) * p.tiles + tile;
+}
+
+// The threads of a block over its groups, `lanes` (a power of two up to 32) neighbours for each group, all groups at
+// once where they fit.  This code and what uses it run once per block: what they cost are latencies and
+// instruction fetches, so all of it is short loops.  (A warp per group, four groups unrolled, and a merge with a
+// division for every pair of results: 3 us of each kernel's 13 to 17.)
+struct GroupLanes {
+    int g0, count, lanes, lane, shift, first, end, step;
+    __device__ __forceinline__ GroupLanes(int first_group, int last_group) {
+        g0 = first_group;
+        count = last_group - first_group + 1;
+        shift = 5;
+        while (shift > 0 && (count << shift) > kTileThreads) --shift;
+        lanes = 1 << shift;
+        lane = threadIdx.x & (lanes - 1);
+        step = kTileThreads >> shift;
+        first = threadIdx.x >> shift;
+        end = (count + step - 1) / step * step;  // every thread takes every step: the sums below need all lanes
+    }
+    __device__ __forceinline__ int group(int k) const { return g0 + min(k, count - 1); }
+    __device__ __forceinline__ bool writes(int k) const { return lane == 0 && k < count; }
+    __device__ __forceinline__ float total(float x) const {
+#pragma unroll 1
+        for (int o = lanes >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        return x;
+    }
+};
+
+// f(a float pair, the number of values behind it) for this lane's pieces of group g over all tiles.
+template <int V, typename F>
+__device__ __forceinline__ void visit_pieces(const NormArgs &p, int n, int g, const GroupLanes &l, int blocks, F f) {
+    const int D = p.C / p.G, cb0 = g * D / (kTileCols * V), cb1 = ((g + 1) * D - 1) / (kTileCols * V);
+#pragma unroll 1
+    for (int cb = cb0; cb <= cb1; ++cb) {
+        const float2 *x = reinterpret_cast<const float2 *>(p.stat_parts) + piece_at(p, n, 0, g, cb, blocks);
+        const float w = (float)(min((g + 1) * D, (cb + 1) * kTileCols * V) - max(g * D, cb * kTileCols * V));
+#pragma unroll 4
+        for (int tile = l.lane; tile < p.tiles; tile += l.lanes) f(x[tile], w * (float)Tile<V>::positions(p, tile));
+    }
+}
 
 template <typename IO, int V>
 __global__ void __launch_bounds__(kTileThreads, 2) norm_tile_stats_kernel(NormArgs p) {
@@ -568,79 +605,71 @@ __global__ void __launch_bounds__(kTileThreads, 2) norm_tile_stats_kernel(NormAr
     extern __shared__ __align__(16) uint8_t ring[];
     PosStream<IO, V, 1> in(p, t, reinterpret_cast<Pack<IO, V> *>(ring));
     in.t[0] = p.x;
-    float mean[V] = {}, m2[V] = {};
+    using U = Unit<V>;
+    constexpr int NU = kUnits<V>;
+    U neg[NU], m2[NU];  // minus the mean, the sum of squares about it
+#pragma unroll
+    for (int u = 0; u < NU; ++u) neg[u] = m2[u] = both<U>(0.f);
     float cnt = 0.f;
     for (in.start(); in.more(); in.next()) {
         Pack<IO, V> x[1];
         in.get(x);
         cnt += 1.f;
-        const float f = __fdividef(1.f, cnt);
+        const U f = both<U>(-__fdividef(1.f, cnt));
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float d = x[0].at(i) - mean[i];
-            mean[i] = fmaf(d, f, mean[i]);
-            m2[i] = fmaf(d, x[0].at(i) - mean[i], m2[i]);
+        for (int u = 0; u < NU; ++u) {
+            const U xu = x[0].unit(u), d = add(xu, neg[u]);
+            neg[u] = fma(d, f, neg[u]);
+            m2[u] = fma(d, add(xu, neg[u]), m2[u]);
         }
     }
-    const int width = t.c1 - t.c0;
-    if (t.live)
+    const int width = t.c1 - t.c0, n = t.s1 - t.s0;
+    if (t.live) {
+        float *mean_to = sh_mean + t.rl * width + t.col * V, *m2_to = sh_m2 + t.rl * width + t.col * V;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            sh_mean[t.rl * width + t.col * V + i] = mean[i];
-            sh_m2[t.rl * width + t.col * V + i] = m2[i];
-        }
-    __syncthreads();
-    // one warp per group piece: the piece's channels times the RL rows of partial results
-    const int lane = threadIdx.x & 31;
-    for (int g = t.first_group(D) + (threadIdx.x >> 5); g <= t.last_group(D); g += kTileThreads / 32) {
-        const int a = max(g * D, t.c0) - t.c0, b = min((g + 1) * D, t.c1) - t.c0;
-        Stat st{0.f, 0.f, 0.f};
-        for (int e = lane; e < (b - a) * t.RL; e += 32) {
-            const int r = e / (b - a), c = a + e % (b - a);
-            const int rows = t.s1 - t.s0 - r;  // positions of row lane r: s0 + r, s0 + r + RL, ...
-            const float n = rows > 0 ? (float)((rows + t.RL - 1) / t.RL) : 0.f;
-            st = merge(st, Stat{n, sh_mean[r * width + c], sh_m2[r * width + c]});
-        }
-        for (int o = 16; o > 0; o >>= 1) st = merge(st, shfl(st, o));
-        if (lane == 0) {
-            float *out = p.stat_parts + 2 * (((long long)blockIdx.x) * norm_pieces(p.G, gridDim.y) + g + t.cb);
-            out[0] = st.mean;
-            out[1] = st.m2;
-        }
-    }
-}
-
-// Visits the pieces of groups g0 .. g0 + 3 (as far as last) over all tiles, by one warp: f(k, a float pair,
-// the number of values behind it) for group g0 + k.  The groups' loads are independent of each other: four
-// at a time, one group after another took 6 us of a 20 us kernel.
-constexpr int kGroupsAtOnce = 4;
-
-template <int V, typename F>
-__device__ __forceinline__ void visit_pieces(const NormArgs &p, int n, int g0, int last, int blocks, F f) {
-    const int D = p.C / p.G, lane = threadIdx.x & 31;
-    int first[kGroupsAtOnce], nb[kGroupsAtOnce], most = 0;
-#pragma unroll
-    for (int k = 0; k < kGroupsAtOnce; ++k) {
-        const int g = g0 + k;
-        first[k] = g * D / (kTileCols * V);
-        nb[k] = g <= last ? ((g + 1) * D - 1) / (kTileCols * V) - first[k] + 1 : 0;
-        most = max(most, nb[k]);
-    }
-    for (int e = lane; e < p.tiles * most; e += 32) {
-        const int tile = e / most, j = e % most;
-        const int rows = (int)((long long)p.S * (tile + 1) / p.tiles) - (int)((long long)p.S * tile / p.tiles);
-        float2 x[kGroupsAtOnce];
-#pragma unroll
-        for (int k = 0; k < kGroupsAtOnce; ++k)
-            if (j < nb[k])
-                x[k] = reinterpret_cast<const float2 *>(p.stat_parts)[((long long)n * p.tiles + tile) * norm_pieces(p.G, blocks) + g0 + k + first[k] + j];
-#pragma unroll
-        for (int k = 0; k < kGroupsAtOnce; ++k)
-            if (j < nb[k]) {
-                const int cb = first[k] + j, g = g0 + k;
-                const int width = min((g + 1) * D, (cb + 1) * kTileCols * V) - max(g * D, cb * kTileCols * V);
-                f(k, x[k], (float)width * (float)rows);
+        for (int u = 0; u < NU; ++u) {
+            if constexpr (V == 1) {
+                mean_to[0] = -neg[0];
+                m2_to[0] = m2[0];
+            } else {
+                mean_to[2 * u] = -first(neg[u]);
+                mean_to[2 * u + 1] = -second(neg[u]);
+                m2_to[2 * u] = first(m2[u]);
+                m2_to[2 * u + 1] = second(m2[u]);
             }
+        }
+    }
+    __syncthreads();
+    // The results of a group piece's channels and row lanes are merged by their mean and the sum of squares about
+    // it: two short sums, of differences from the first of them, so that equal values have exactly their mean.
+    const GroupLanes l(t.first_group(D), t.last_group(D));
+    const int per = n / t.RL, more = n - per * t.RL;  // positions of a row lane, and how many lanes have one more
+    for (int k = l.first; k < l.end; k += l.step) {
+        const int g = l.group(k);
+        const int a = max(g * D, t.c0) - t.c0, w = min((g + 1) * D, t.c1) - t.c0 - a;
+        const int r0 = l.lane / w, c0 = l.lane - r0 * w, dr = l.lanes / w, dc = l.lanes - dr * w;
+        auto visit = [&](auto f) {
+#pragma unroll 2
+            for (int r = r0, c = c0; r < t.RL;) {
+                f(r * width + a + c, (float)(per + (r < more)));
+                r += dr;
+                c += dc;
+                if (c >= w) {
+                    c -= w;
+                    ++r;
+                }
+            }
+        };
+        const float m0 = sh_mean[a];
+        float sum = 0.f, sq = 0.f;
+        visit([&](int e, float cnt) { sum = fmaf(cnt, sh_mean[e] - m0, sum); });
+        const float mean = m0 + __fdividef(l.total(sum), (float)w * (float)n);
+        visit([&](int e, float cnt) {
+            const float d = sh_mean[e] - mean;
+            sq += fmaf(cnt * d, d, sh_m2[e]);
+        });
+        sq = l.total(sq);
+        if (l.writes(k)) reinterpret_cast<float2 *>(p.stat_parts)[piece_at(p, t.n, t.tile, g, t.cb, gridDim.y)] = make_float2(mean, sq);
     }
 }
 
@@ -654,42 +683,76 @@ __global__ void __launch_bounds__(kTileThreads, 2) norm_tile_apply_kernel(NormAr
     in.t[0] = p.x;
     in.t[1] = mode_gate<MODE>(p) ? p.gate : nullptr;
     in.start();
-    dependent_wait();
-    for (int g = g0 + kGroupsAtOnce * (threadIdx.x >> 5); g <= t.last_group(D); g += kGroupsAtOnce * (kTileThreads / 32)) {
-        Stat st[kGroupsAtOnce] = {};
-        visit_pieces<V>(p, t.n, g, t.last_group(D), gridDim.y,
-                        [&](int k, const float2 &x, float count) { st[k] = merge(st[k], Stat{count, x.x, x.y}); });
+    using U = Unit<V>;
+    constexpr int NU = kUnits<V>;
+    float w[V];
+    U scale[NU], shift[NU];
 #pragma unroll
-        for (int k = 0; k < kGroupsAtOnce; ++k) {
-            for (int o = 16; o > 0; o >>= 1) st[k] = merge(st[k], shfl(st[k], o));
-            if ((threadIdx.x & 31) == 0 && g + k <= t.last_group(D)) {
-                const float rstd = rsqrtf(st[k].m2 / ((float)D * (float)p.S) + p.eps);
-                sh_mean[g + k - g0] = st[k].mean;
-                sh_rstd[g + k - g0] = rstd;
-                if (t.tile == 0 && (g + k) * D >= t.c0) {  // the block with the group's first channel
-                    if (p.mean) p.mean[(long long)t.n * p.G + g + k] = st[k].mean;
-                    if (p.rstd) p.rstd[(long long)t.n * p.G + g + k] = rstd;
-                }
+    for (int i = 0; i < V; ++i) w[i] = p.weight && t.live ? p.weight[t.c0 + t.col * V + i] : 1.f;
+#pragma unroll
+    for (int u = 0; u < NU; ++u) shift[u] = channel_unit<V>(t.live ? p.bias : nullptr, t.c0 + t.col * V + 2 * u, 0.f);
+    dependent_wait();
+    const GroupLanes l(g0, t.last_group(D));
+    const float count = (float)D * (float)p.S;
+    for (int k = l.first; k < l.end; k += l.step) {
+        const int g = l.group(k);
+        const float m0 = p.stat_parts[2 * piece_at(p, t.n, 0, g, g * D / (kTileCols * V), gridDim.y)];
+        float sum = 0.f, sq = 0.f;
+        visit_pieces<V>(p, t.n, g, l, gridDim.y, [&](const float2 &x, float n) { sum = fmaf(n, x.x - m0, sum); });
+        const float mean = m0 + __fdividef(l.total(sum), count);
+        visit_pieces<V>(p, t.n, g, l, gridDim.y, [&](const float2 &x, float n) {
+            const float d = x.x - mean;
+            sq += fmaf(n * d, d, x.y);
+        });
+        const float rstd = rsqrtf(__fdividef(l.total(sq), count) + p.eps);
+        if (l.writes(k)) {
+            sh_mean[g - g0] = mean;
+            sh_rstd[g - g0] = rstd;
+            if (t.tile == 0 && g * D >= t.c0) {  // the block with the group's first channel
+                if (p.mean) p.mean[(long long)t.n * p.G + g] = mean;
+                if (p.rstd) p.rstd[(long long)t.n * p.G + g] = rstd;
             }
         }
     }
     __syncthreads();
     if (!t.live) return;
-    float mean[V], rstd[V], w[V], b[V];
+    int g = (t.c0 + t.col * V) / D;
+    U neg[NU];  // z = (x + neg) scale + shift
+    float m[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = t.c0 + t.col * V + i, g = c / D - g0;
-        mean[i] = sh_mean[g];
-        rstd[i] = sh_rstd[g];
-        w[i] = p.weight ? p.weight[c] : 1.f;
-        b[i] = p.bias ? p.bias[c] : 0.f;
+        if (t.c0 + t.col * V + i >= (g + 1) * D) ++g;
+        m[i] = -sh_mean[g - g0];
+        w[i] *= sh_rstd[g - g0];
+    }
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+        neg[u] = unit_of<V>(m, u);
+        scale[u] = unit_of<V>(w, u);
     }
     for (; in.more(); in.next()) {
         Pack<IO, V> x[2], y;
         in.get(x);
 #pragma unroll
-        for (int i = 0; i < V; ++i) st_io(y.v, i, y_of<IO, MODE>(p, fmaf((x[0].at(i) - mean[i]) * rstd[i], w[i], b[i]), x[1].at(i)));
+        for (int u = 0; u < NU; ++u) y.set(u, y_of<IO, MODE>(p, fma(add(x[0].unit(u), neg[u]), scale[u], shift[u]), x[1].unit(u)));
         store_pack<IO, V>(p.y, in.at, y);
+    }
+}
+
+// What the backward pass needs of a thread's channels, the first of them in group g.
+template <int V>
+__device__ __forceinline__ void norm_params(const NormArgs &p, const Tile<V> &t, int g, float (&mean)[V], float (&rstd)[V], float (&w)[V],
+                                            float (&b)[V]) {
+    const int D = p.C / p.G;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = t.c0 + t.col * V + i;
+        if (c >= (g + 1) * D) ++g;
+        const bool in = t.live;
+        mean[i] = in ? p.mean[(long long)t.n * p.G + g] : 0.f;
+        rstd[i] = in ? p.rstd[(long long)t.n * p.G + g] : 0.f;
+        w[i] = in && p.weight ? p.weight[c] : 1.f;
+        b[i] = in && p.bias ? p.bias[c] : 0.f;
     }
 }
 
@@ -715,14 +778,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) norm_tile_grad_sums_kernel(No
         __syncthreads();
         if (t.live) {
             float mean[V], rstd[V], w[V], b[V], sz[V] = {}, szx[V] = {};
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int c = t.c0 + t.col * V + i;
-                mean[i] = p.mean[(long long)t.n * p.G + c / D];
-                rstd[i] = p.rstd[(long long)t.n * p.G + c / D];
-                w[i] = p.weight ? p.weight[c] : 1.f;
-                b[i] = p.bias ? p.bias[c] : 0.f;
-            }
+            norm_params<V>(p, t, (t.c0 + t.col * V) / D, mean, rstd, w, b);
             for (; in.more(); in.next()) {
                 Pack<IO, V> x[3];
                 in.get(x);
@@ -755,21 +811,19 @@ __global__ void __launch_bounds__(kTileThreads, 2) norm_tile_grad_sums_kernel(No
             sh2[c] = b * w;
         }
         __syncthreads();
-        const int lane = threadIdx.x & 31;
-        for (int g = t.first_group(D) + (threadIdx.x >> 5); g <= t.last_group(D); g += kTileThreads / 32) {
+        const GroupLanes l(t.first_group(D), t.last_group(D));
+        for (int k = l.first; k < l.end; k += l.step) {
+            const int g = l.group(k);
             const int a = max(g * D, t.c0) - t.c0, b = min((g + 1) * D, t.c1) - t.c0;
             float s1 = 0.f, s2 = 0.f;
-            for (int c = a + lane; c < b; c += 32) {
+#pragma unroll 2
+            for (int c = a + l.lane; c < b; c += l.lanes) {
                 s1 += sh1[c];
                 s2 += sh2[c];
             }
-            s1 = warp_sum(s1);
-            s2 = warp_sum(s2);
-            if (lane == 0) {
-                float *out = p.stat_parts + 2 * ((long long)unit * norm_pieces(p.G, gridDim.y) + g + t.cb);
-                out[0] = s1;
-                out[1] = s2;
-            }
+            s1 = l.total(s1);
+            s2 = l.total(s2);
+            if (l.writes(k)) reinterpret_cast<float2 *>(p.stat_parts)[piece_at(p, t.n, t.tile, g, t.cb, gridDim.y)] = make_float2(s1, s2);
         }
     }
     if (!p.chan_parts) return;
@@ -785,40 +839,39 @@ template <typename IO, int V, int MODE>
 __global__ void __launch_bounds__(kTileThreads, 2) norm_tile_grad_apply_kernel(NormArgs p) {
     __shared__ float sh1[kTileCols * V], sh2[kTileCols * V];
     const Tile<V> t(p, blockIdx.x);
-    const int D = p.C / p.G, g0 = t.first_group(D), lane = threadIdx.x & 31;
+    const int D = p.C / p.G, g0 = t.first_group(D);
     extern __shared__ __align__(16) uint8_t ring[];
     PosStream<IO, V, 3> in(p, t, reinterpret_cast<Pack<IO, V> *>(ring));
     in.t[0] = p.x;
     in.t[1] = p.dy;
     in.t[2] = mode_gate<MODE>(p) ? p.gate : nullptr;
     in.start();
+    const int g_first = (t.c0 + t.col * V) / D;
+    float mean[V], rstd[V], w[V], b[V], s1[V], s2[V];
+    norm_params<V>(p, t, g_first, mean, rstd, w, b);
     dependent_wait();
     const float inv = 1.f / ((float)D * (float)p.S);
-    for (int g = g0 + kGroupsAtOnce * (threadIdx.x >> 5); g <= t.last_group(D); g += kGroupsAtOnce * (kTileThreads / 32)) {
-        float2 sum[kGroupsAtOnce] = {};
-        visit_pieces<V>(p, t.n, g, t.last_group(D), gridDim.y, [&](int k, const float2 &x, float) {
-            sum[k].x += x.x;
-            sum[k].y += x.y;
+    const GroupLanes l(g0, t.last_group(D));
+    for (int k = l.first; k < l.end; k += l.step) {
+        const int g = l.group(k);
+        float a = 0.f, b = 0.f;
+        visit_pieces<V>(p, t.n, g, l, gridDim.y, [&](const float2 &x, float) {
+            a += x.x;
+            b += x.y;
         });
-#pragma unroll
-        for (int k = 0; k < kGroupsAtOnce; ++k) {
-            const float a = warp_sum(sum[k].x), b = warp_sum(sum[k].y);
-            if (lane == 0 && g + k <= t.last_group(D)) {
-                sh1[g + k - g0] = a * inv;
-                sh2[g + k - g0] = b * inv;
-            }
+        a = l.total(a);
+        b = l.total(b);
+        if (l.writes(k)) {
+            sh1[g - g0] = a * inv;
+            sh2[g - g0] = b * inv;
         }
     }
     __syncthreads();
     if (!t.live) return;
-    float mean[V], rstd[V], w[V], b[V], s1[V], s2[V];
+    int g = g_first;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = t.c0 + t.col * V + i, g = c / D;
-        mean[i] = p.mean[(long long)t.n * p.G + g];
-        rstd[i] = p.rstd[(long long)t.n * p.G + g];
-        w[i] = p.weight ? p.weight[c] : 1.f;
-        b[i] = p.bias ? p.bias[c] : 0.f;
+        if (t.c0 + t.col * V + i >= (g + 1) * D) ++g;
         s1[i] = sh1[g - g0];
         s2[i] = sh2[g - g0];
     }
@@ -982,6 +1035,10 @@ NormArgs args_of(const prism_norm_shape &s, const NormPlan &pl, const void *x, c
     a.N = s.N; a.S = s.S; a.C = s.C; a.G = s.G; a.act = s.act; a.eps = s.eps;
     a.x = x; a.gate = gate; a.weight = weight; a.bias = bias;
     a.tiles = pl.tiles;
+    if (pl.tiles > 0) {
+        a.tile_len = s.S / pl.tiles;
+        a.tile_more = s.S % pl.tiles;
+    }
     return a;
 }
 
