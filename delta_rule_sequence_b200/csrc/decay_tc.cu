@@ -211,8 +211,16 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
     const uint32_t lim = p.stall ? kStallPolls : kPolls;
     const float a = p.decay[wk.h];
 
+    auto load = [&](int i) {
+        const int st = i % NST;
+        uint8_t *s = sm + st * LY::STAGE;
+        mbar_expect_tx(&full[st], LY::STAGE);
+        for (int c = 0; c < D1 / 64; ++c) tma_load_4d(s + c * kBlk, &maps.y, 64 * c, wk.h / p.y.div, wk.t0(i), wk.b, &full[st]);
+        for (int c = 0; c < D2 / 64; ++c)
+            tma_load_4d(s + tile_bytes<D1>() + c * kBlk, &maps.z, 64 * c, wk.h / p.z.div, wk.t0(i), wk.b, &full[st]);
+    };
     if (warp == LY::MMAW) tmem_alloc(&tmem_base_sh, 512);
-    if (tid == 0) {
+    if (warp == LY::LOADW && lane == 0) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&freeb[i], LY::YW + 1);
@@ -225,6 +233,8 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
         mbar_init(&d_free, LY::SW);
         mbar_init(&drain, 1);
         mbar_fence_init();
+        // the first loads are on their way while the others set up
+        for (int i = 0; i < NST && i < wk.nch && !p.stall; ++i) load(i);
     }
     pw.fill(a, wk.reverse, tid, LY::THREADS);
     fence_before_sync();
@@ -238,15 +248,10 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
 
     if (warp == LY::LOADW) {
         if (lane == 0 && !p.stall) {
-            int i = 0;
+            int i = min(NST, wk.nch);
             for (; i < wk.nch; ++i) {
-                const int st = i % NST;
-                if (i >= NST && !mbar_wait_suspend(&freeb[st], (uint32_t)((i / NST - 1) & 1), status, lim)) break;
-                uint8_t *s = sm + st * LY::STAGE;
-                mbar_expect_tx(&full[st], LY::STAGE);
-                for (int c = 0; c < D1 / 64; ++c) tma_load_4d(s + c * kBlk, &maps.y, 64 * c, wk.h / p.y.div, wk.t0(i), wk.b, &full[st]);
-                for (int c = 0; c < D2 / 64; ++c)
-                    tma_load_4d(s + tile_bytes<D1>() + c * kBlk, &maps.z, 64 * c, wk.h / p.z.div, wk.t0(i), wk.b, &full[st]);
+                if (!mbar_wait_suspend(&freeb[i % NST], (uint32_t)((i / NST - 1) & 1), status, lim)) break;
+                load(i);
             }
             // loads in flight land before the CTA exits
             for (int k = i > NST ? i - NST : 0; k < i; ++k) mbar_wait_suspend(&full[k % NST], (uint32_t)((k / NST) & 1), nullptr, lim);
@@ -394,8 +399,12 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
     const uint32_t lim = p.stall ? kStallPolls : kPolls;
     const float a = p.decay[wk.h];
 
+    auto load_x = [&](int i) { load_tile(sm + i % NST * LY::STAGE + LY::X, &maps.x, D1, wk.h / p.x.div, wk.t0(i), wk.b, &x_full[i % NST]); };
+    auto load_y = [&](int i) { load_tile(sm + i % NST * LY::STAGE + LY::Y, &maps.y, D1, wk.h / p.y.div, wk.t0(i), wk.b, &y_full[i % NST]); };
+    auto load_z = [&](int i) { load_tile(sm + i % NST * LY::STAGE + LY::Z, &maps.z, D2, wk.h / p.z.div, wk.t0(i), wk.b, &z_full[i % NST]); };
+    const int early = p.stall ? 0 : min(NST, wk.nch);
     if (warp == LY::MMAW) tmem_alloc(&tmem_base_sh, 512);
-    if (tid == 0) {
+    if (warp == LY::LOADW && lane == 0) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(&x_full[i], 1);
             mbar_init(&y_full[i], 1);
@@ -416,6 +425,12 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
         mbar_init(&yp_free, 1);
         mbar_init(&drain, 1);
         mbar_fence_init();
+        // the first loads are on their way while the others set up
+        for (int i = 0; i < early; ++i) {
+            load_x(i);
+            load_y(i);
+            load_z(i);
+        }
     }
     pw.fill(a, wk.reverse, tid, LY::THREADS);
     fence_before_sync();
@@ -426,21 +441,18 @@ __global__ void __launch_bounds__(PassLayout<D1, D2>::THREADS, 1)
     if (warp >= LY::LOADW) setmaxnreg_dec<LY::RM>();
     if (warp == LY::LOADW) {
         if (lane == 0 && !p.stall) {
-            int i = 0;
-            bool ok = true;
-            int nx = 0, ny = 0, nz = 0;  // tiles requested
-            for (; i < wk.nch && ok; ++i) {
+            int nx = early, ny = early, nz = early;  // tiles requested
+            for (int i = early; i < wk.nch; ++i) {
                 const int st = i % NST;
                 const uint32_t par = (uint32_t)((i / NST - 1) & 1);
-                uint8_t *s = sm + st * LY::STAGE;
-                if (i >= NST && !mbar_wait_suspend(&x_free[st], par, status, lim)) { ok = false; break; }
-                load_tile(s + LY::X, &maps.x, D1, wk.h / p.x.div, wk.t0(i), wk.b, &x_full[st]);
+                if (!mbar_wait_suspend(&x_free[st], par, status, lim)) break;
+                load_x(i);
                 ++nx;
-                if (i >= NST && !mbar_wait_suspend(&y_free[st], par, status, lim)) { ok = false; break; }
-                load_tile(s + LY::Y, &maps.y, D1, wk.h / p.y.div, wk.t0(i), wk.b, &y_full[st]);
+                if (!mbar_wait_suspend(&y_free[st], par, status, lim)) break;
+                load_y(i);
                 ++ny;
-                if (i >= NST && !mbar_wait_suspend(&z_free[st], par, status, lim)) { ok = false; break; }
-                load_tile(s + LY::Z, &maps.z, D2, wk.h / p.z.div, wk.t0(i), wk.b, &z_full[st]);
+                if (!mbar_wait_suspend(&z_free[st], par, status, lim)) break;
+                load_z(i);
                 ++nz;
             }
             // loads in flight land before the CTA exits
