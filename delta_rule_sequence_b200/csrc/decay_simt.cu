@@ -61,28 +61,72 @@ __device__ __forceinline__ void state_tile(const float *Y, const float *Z, const
     }
 }
 
-// o[r][c] += sum_k A[row r][k] B[k][n0 + c], rows ty + 16 r of A (pitch pa), K a multiple of 4.
-template <int D2>
-__device__ __forceinline__ void rows_tile(const float *A, int pa, const float *B, int K, F2 (&o)[4][D2 / 32]) {
+// o[r][c] += sum over k in [K0, K1) of A[row r][k] B[k][n0 + c], rows ty + 16 r of A (pitch pa), R0 <= r < R1.
+template <int D2, int R0, int R1>
+__device__ __forceinline__ void rows_range(const float *A, int pa, const float *B, int K0, int K1, F2 (&o)[4][D2 / 32]) {
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll 2
-    for (int k0 = 0; k0 < K; k0 += 4) {
+    for (int k0 = K0; k0 < K1; k0 += 4) {
         float4 a[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) a[r] = *reinterpret_cast<const float4 *>(A + (ty + 16 * r) * pa + k0);
+        for (int r = R0; r < R1; ++r) a[r] = *reinterpret_cast<const float4 *>(A + (ty + 16 * r) * pa + k0);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             F2 b[D2 / 64][2];
 #pragma unroll
             for (int i = 0; i < D2 / 64; ++i) lds4(B + (k0 + k) * (D2 + 4) + 64 * i + 4 * tx, b[i]);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
+            for (int r = R0; r < R1; ++r) {
                 const float x = (&a[r].x)[k];
                 const F2 xx = pack2(x, x);
 #pragma unroll
                 for (int c = 0; c < D2 / 32; ++c) o[r][c] = fma(xx, b[c >> 1][c & 1], o[r][c]);
             }
         }
+    }
+}
+
+// The chunk's own part of a pass: P[i][j] = a^|i-j| x_i . y_j on the causal side, rows i = ty + 16 r, columns
+// j = tx + 16 c.  Of the 16 x 16 blocks those on the other side are skipped, here and in P Z: 6 of 16.
+// (REV: the causal side is j >= i.)
+template <int D1, bool REV>
+__device__ __forceinline__ void scores(const float *X, const float *Y, const float *pw, float *P) {
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    F2 s2[4][4] = {};  // sums over even and odd columns
+#pragma unroll 2
+    for (int d = 0; d < D1; d += 4) {
+        F2 xv[4][2], yv[4][2];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            lds4(X + (ty + 16 * r) * (D1 + 4) + d, xv[r]);
+            lds4(Y + (tx + 16 * r) * (D1 + 4) + d, yv[r]);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int c = REV ? r : 0; c < (REV ? 4 : r + 1); ++c) s2[r][c] = fma(xv[r][0], yv[c][0], fma(xv[r][1], yv[c][1], s2[r][c]));
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = REV ? r : 0; c < (REV ? 4 : r + 1); ++c) {
+            const int i = ty + 16 * r, j = tx + 16 * c, gap = REV ? j - i : i - j;
+            P[i * (CH + 4) + j] = gap >= 0 ? total(s2[r][c]) * pw[gap] : 0.f;
+        }
+}
+template <int D2, bool REV>
+__device__ __forceinline__ void causal_rows(const float *P, const float *Z, F2 (&o)[4][D2 / 32]) {
+    constexpr int PP = CH + 4;
+    if constexpr (REV) {
+        rows_range<D2, 0, 1>(P, PP, Z, 0, 16, o);
+        rows_range<D2, 0, 2>(P, PP, Z, 16, 32, o);
+        rows_range<D2, 0, 3>(P, PP, Z, 32, 48, o);
+        rows_range<D2, 0, 4>(P, PP, Z, 48, 64, o);
+    } else {
+        rows_range<D2, 0, 4>(P, PP, Z, 0, 16, o);
+        rows_range<D2, 1, 4>(P, PP, Z, 16, 32, o);
+        rows_range<D2, 2, 4>(P, PP, Z, 32, 48, o);
+        rows_range<D2, 3, 4>(P, PP, Z, 48, 64, o);
     }
 }
 
@@ -169,10 +213,8 @@ __global__ void __launch_bounds__(NT) decay_sum_simt_kernel(const __grid_constan
 template <int D1, int D2>
 __global__ void __launch_bounds__(NT) decay_pass_simt_kernel(const __grid_constant__ DecayPassSet set) {
     extern __shared__ __align__(16) float sm[];
-    constexpr int PP = CH + 4;
     using SZ = PassSizes<D1, D2>;
-    float *R = sm + SZ::NB * SZ::SET, *P = R + D1 * (D2 + 4), *pw = P + CH * PP, *w = pw + CH + 1;
-    dependent_wait();
+    float *R = sm + SZ::NB * SZ::SET, *P = R + D1 * (D2 + 4), *pw = P + CH * (CH + 4), *w = pw + CH + 1;
     const DecayPass &p = set.p[blockIdx.x / set.p[0].nseg];
     const int seg = blockIdx.x % p.nseg, h = blockIdx.y, b = blockIdx.z;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -180,15 +222,6 @@ __global__ void __launch_bounds__(NT) decay_pass_simt_kernel(const __grid_consta
     const int s0 = seg * p.seg_tokens;
     const int send = min(s0 + p.seg_tokens, p.T), s1 = min(send, len);
     const float a = p.decay[h];
-    for (int i = threadIdx.x; i <= CH; i += NT) pw[i] = decay_pow(a, i);
-    const float *E = p.entry ? p.entry + (((long long)b * p.H + h) * p.nseg + seg) * p.d1 * p.d2 : nullptr;
-    for (int e = threadIdx.x; e < D1 * D2; e += NT) {
-        // m fastest where R's rows are along y (n * d1 + m), n fastest otherwise
-        const int m = p.entry_t ? e / D2 : e % D1, n = p.entry_t ? e % D2 : e / D1;
-        float x = 0.f;
-        if (E && m < p.d1 && n < p.d2) x = E[p.entry_t ? m * p.d2 + n : n * p.d1 + m];
-        R[m * (D2 + 4) + n] = x;
-    }
     const int nch = s1 > s0 ? (s1 - s0 + CH - 1) / CH : 0;
     auto token = [&](int cc) { return s0 + (p.reverse ? nch - 1 - cc : cc) * CH; };
     auto request = [&](int cc) {
@@ -199,6 +232,21 @@ __global__ void __launch_bounds__(NT) decay_pass_simt_kernel(const __grid_consta
         request_commit();
     };
     if (SZ::NB == 2 && nch > 0) request(0);
+    for (int i = threadIdx.x; i <= CH; i += NT) pw[i] = decay_pow(a, i);
+    // (the entry state comes from the call's previous kernel; all that was read so far is older than the call)
+    dependent_wait();
+    const float *E = p.entry ? p.entry + (((long long)b * p.H + h) * p.nseg + seg) * p.d1 * p.d2 : nullptr;
+#pragma unroll 4
+    for (int e = threadIdx.x; e < D1 * D2 / 4; e += NT) {  // four values of one row of R at a time
+        // rows of E along z (m * d2 + n): n fastest; along y (n * d1 + m): m fastest
+        const int m = p.entry_t ? e / (D2 / 4) : e % D1, n = 4 * (p.entry_t ? e % (D2 / 4) : e / D1);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (E && m < p.d1 && n < p.d2) {  // (widths are multiples of 32)
+            if (p.entry_t) x = *reinterpret_cast<const float4 *>(E + m * p.d2 + n);
+            else x = make_float4(E[n * p.d1 + m], E[(n + 1) * p.d1 + m], E[(n + 2) * p.d1 + m], E[(n + 3) * p.d1 + m]);
+        }
+        *reinterpret_cast<float4 *>(R + m * (D2 + 4) + n) = x;
+    }
     for (int cc = 0; cc < nch; ++cc) {
         const int t0 = token(cc), n = min(CH, s1 - t0);
         const float *X = sm + (cc % SZ::NB) * SZ::SET, *Y = X + CH * (D1 + 4), *Z = Y + CH * (D1 + 4);
@@ -212,34 +260,12 @@ __global__ void __launch_bounds__(NT) decay_pass_simt_kernel(const __grid_consta
         }
         for (int j = threadIdx.x; j < CH; j += NT) w[j] = j < n ? pw[write_exponent(j, n, p.reverse)] : 0.f;
         __syncthreads();
-        // P[i][j] = a^|i-j| x_i . y_j on the causal side, rows i = ty + 16 r, columns j = tx + 16 c
-        {
-            F2 s2[4][4] = {};  // sums over even and odd columns
-#pragma unroll 2
-            for (int d = 0; d < D1; d += 4) {
-                F2 xv[4][2], yv[4][2];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    lds4(X + (ty + 16 * r) * (D1 + 4) + d, xv[r]);
-                    lds4(Y + (tx + 16 * r) * (D1 + 4) + d, yv[r]);
-                }
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) s2[r][c] = fma(xv[r][0], yv[c][0], fma(xv[r][1], yv[c][1], s2[r][c]));
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int i = ty + 16 * r, j = tx + 16 * c, gap = p.reverse ? j - i : i - j;
-                    P[i * PP + j] = gap >= 0 ? total(s2[r][c]) * pw[gap] : 0.f;
-                }
-        }
+        if (p.reverse) scores<D1, true>(X, Y, pw, P);
+        else scores<D1, false>(X, Y, pw, P);
         __syncthreads();
         F2 o[4][D2 / 32] = {};
         // entry term, then scaled by its row's decay, then the chunk's own
-        rows_tile<D2>(X, D1 + 4, R, D1, o);
+        rows_range<D2, 0, 4>(X, D1 + 4, R, 0, D1, o);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int i = ty + 16 * r;
@@ -247,7 +273,8 @@ __global__ void __launch_bounds__(NT) decay_pass_simt_kernel(const __grid_consta
 #pragma unroll
             for (int c = 0; c < D2 / 32; ++c) o[r][c] = mul(o[r][c], pack2(f, f));
         }
-        rows_tile<D2>(P, PP, Z, CH, o);
+        if (p.reverse) causal_rows<D2, true>(P, Z, o);
+        else causal_rows<D2, false>(P, Z, o);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int i = ty + 16 * r;
