@@ -41,7 +41,7 @@ __device__ __forceinline__ void lds4(const float *p, F2 (&v)[2]) {
 template <int D1, int D2>
 __device__ __forceinline__ void state_tile(const float *Y, const float *Z, const float *w, F2 (&acc)[D1 / 16][D2 / 32]) {
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-#pragma unroll 2
+#pragma unroll 4
     for (int j = 0; j < CH; ++j) {
         const float wj = w[j];
         F2 z[D2 / 64][2];
@@ -65,7 +65,7 @@ __device__ __forceinline__ void state_tile(const float *Y, const float *Z, const
 template <int D2, int R0, int R1>
 __device__ __forceinline__ void rows_range(const float *A, int pa, const float *B, int K0, int K1, F2 (&o)[4][D2 / 32]) {
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-#pragma unroll 2
+#pragma unroll 4
     for (int k0 = K0; k0 < K1; k0 += 4) {
         float4 a[4];
 #pragma unroll
@@ -93,7 +93,7 @@ template <int D1, bool REV>
 __device__ __forceinline__ void scores(const float *X, const float *Y, const float *pw, float *P) {
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     F2 s2[4][4] = {};  // sums over even and odd columns
-#pragma unroll 2
+#pragma unroll 4
     for (int d = 0; d < D1; d += 4) {
         F2 xv[4][2], yv[4][2];
 #pragma unroll
@@ -165,7 +165,6 @@ __global__ void __launch_bounds__(NT) decay_sum_simt_kernel(const __grid_constan
     const int s0 = seg * p.seg_tokens;
     const int s1 = min(s0 + p.seg_tokens, len);
     const float a = p.decay[h];
-    for (int i = threadIdx.x; i <= CH; i += NT) pw[i] = decay_pow(a, i);
     F2 acc[D1 / 16][D2 / 32] = {};
     const int nch = s1 > s0 ? (s1 - s0 + CH - 1) / CH : 0;
     auto token = [&](int cc) { return s0 + (p.reverse ? nch - 1 - cc : cc) * CH; };
@@ -176,6 +175,7 @@ __global__ void __launch_bounds__(NT) decay_sum_simt_kernel(const __grid_constan
         request_commit();
     };
     if (nch > 0) request(0);
+    for (int i = threadIdx.x; i <= CH; i += NT) pw[i] = decay_pow(a, i);
     for (int cc = 0; cc < nch; ++cc) {
         const int n = min(CH, s1 - token(cc));
         const float *Y = sm + (cc % SZ::NB) * SZ::SET, *Z = Y + CH * (D1 + 4);
