@@ -43,14 +43,18 @@ __device__ __forceinline__ void state_tile(const float *Y, const float *Z, const
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll 4
     for (int j = 0; j < CH; ++j) {
-        const float wj = w[j];
+        const F2 ww = pack2(w[j], w[j]);
         F2 z[D2 / 64][2];
 #pragma unroll
-        for (int i = 0; i < D2 / 64; ++i) lds4(Z + j * (D2 + 4) + 64 * i + 4 * tx, z[i]);
+        for (int i = 0; i < D2 / 64; ++i) {
+            lds4(Z + j * (D2 + 4) + 64 * i + 4 * tx, z[i]);
+            z[i][0] = mul(z[i][0], ww);
+            z[i][1] = mul(z[i][1], ww);
+        }
 #pragma unroll
         for (int i = 0; i < D1 / 64; ++i) {
             const float4 y = *reinterpret_cast<const float4 *>(Y + j * (D1 + 4) + 64 * i + 4 * ty);
-            const float yf[4] = {y.x * wj, y.y * wj, y.z * wj, y.w * wj};
+            const float yf[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const F2 yy = pack2(yf[r], yf[r]);
