@@ -178,9 +178,15 @@ __device__ __forceinline__ void zero_rows(uint8_t *tile, int n, int tid, int nth
 
 template <int D1, int D2>
 struct SumLayout {
-    static constexpr int YW = 8, SW = 8;                 // warps that weigh Y, that hold the state
+    // Warps that weigh Y, that hold the state.  (8 for Y: 2 % slower on 16 heads of 65536 tokens of 128, 3 % on a padded
+    // batch of 64-wide heads.)
+    static constexpr int YW = 16, SW = 8;
     static constexpr int LOADW = YW + SW, MMAW = LOADW + 1;
-    static constexpr int THREADS = 32 * (MMAW + 1);
+    static constexpr int THREADS = 32 * (LOADW + 4);     // whole warpgroups: two warps of the last have no role
+    // Registers of a thread by role, as in the pass (launched with 72).
+    static constexpr int RS = 112, RY = 56, RM = 40;
+    static constexpr int SHARES = (SW * RS + YW * RY + 4 * RM) * 32;
+    static_assert(THREADS == 896 && SHARES <= 72 * THREADS, "register shares");
     // The weighted Y: two buffers of three terms in TMEM, or (D1 = 64) one or two in shared memory.
     static constexpr int NYB = D1 == 64 && D2 == 128 ? 1 : 2;
     static constexpr int NST = 3;
@@ -246,6 +252,7 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
             w_last[j] = wk.reverse ? pw.w[j] : pw.at(max(wk.n(wk.nch - 1) - 1 - j, 0));
     __syncthreads();
 
+    if (warp >= LY::LOADW) setmaxnreg_dec<LY::RM>();
     if (warp == LY::LOADW) {
         if (lane == 0 && !p.stall) {
             int i = min(NST, wk.nch);
@@ -288,8 +295,11 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
             mma_commit_warp(&drain);
             mbar_wait_suspend(&drain, 0, nullptr, lim);
         }
+    } else if (warp > LY::MMAW) {
+        // (no role)
     } else if (warp < LY::YW) {
-        const int q = warp & 3, half = warp >> 2, m = 32 * q + lane;
+        setmaxnreg_dec<LY::RY>();
+        const int q = warp & 3, j1 = CT / (LY::YW / 4) * (warp >> 2), m = 32 * q + lane;
         for (int i = 0; i < wk.nch; ++i) {
             const int st = i % NST, pb = i % LY::NYB, n = wk.n(i);
             uint8_t *s = sm + st * LY::STAGE;
@@ -303,7 +313,7 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
                 weigh_tile64<3>(s, sm + LY::YP + pb * LY::YP_BYTES, w, n, tid, 32 * LY::YW);
             } else {
 #pragma unroll 1
-                for (int j0 = 64 * half; j0 < 64 * half + 64; j0 += kWeigh)
+                for (int j0 = j1; j0 < j1 + CT / (LY::YW / 4); j0 += kWeigh)
                     weigh<3>(s, m, w, j0, n, taddr(tb, 32 * q, 0), LY::cY + pb * 192);
                 tmem_wait_st();
             }
@@ -316,6 +326,7 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
             }
         }
     } else {
+        setmaxnreg_inc<LY::RS>();
         const int sw = warp - LY::YW, q = sw & 3, half = sw >> 2, m = product_row<D1>(q, lane);
         constexpr int NC = D2 / 2;
         float r[NC];
@@ -793,7 +804,7 @@ cudaError_t launch_one(const DecayPassSet &set, bool sum, cudaStream_t s) {
         if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return err;
         cudaFuncAttributes attr;
         if ((err = cudaFuncGetAttributes(&attr, kern)) != cudaSuccess) return err;
-        if (!sum && attr.numRegs * threads < PassLayout<D1, D2>::SHARES) return cudaErrorInvalidKernelImage;
+        if (attr.numRegs * threads < (sum ? (int)SumLayout<D1, D2>::SHARES : (int)PassLayout<D1, D2>::SHARES)) return cudaErrorInvalidKernelImage;
         if (dev < 64) ready[sum][dev] = true;
     }
     return dependent_launch(kern, dim3(set.count * p.nseg, p.H, p.B), threads, bytes, s, set.dependent, set, maps);
