@@ -409,13 +409,17 @@ def prism_scan_fwd_launch_count(shape: PrismShape) -> int:
 
 def prism_query_device_status(workspace, stream=None, device=None) -> int:
     """Synchronise and return (and clear) the status words: the one kernels wrote into
-    `workspace` (or None), and the library's own (decode, producer, no-alloc scratch) on the
-    workspace's device (else `device`, else the current device)."""
+    `workspace` (or None), and the library's own (decode, producer, decay scan, no-alloc scratch) on
+    the workspace's device (else `device`, else the stream's, else the current device)."""
     if workspace is not None:
         device = workspace.device
     elif device is None:
-        device = stream.device if stream is not None else torch.device("cuda", torch.cuda.current_device())
+        device = stream.device if stream is not None else "cuda"
     device = torch.device(device)
+    if device.type != "cuda":
+        raise ValueError(f"status words are kept on CUDA devices, got {device}")
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
     return _call(device, load_library().prism_query_device_status, _ptr(workspace),
                  _stream(stream, device))
 
