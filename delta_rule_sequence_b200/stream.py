@@ -120,8 +120,10 @@ class StreamingScan:
             raise ValueError("a gate needs a stream with a norm_fn")
         entry = self.counter.state(self.S0)
         o, _ = self.scan(q, k, v, alpha, beta, u, w, entry, self.chunk)
+        if self.norm is not None:
+            o = self.norm(o, gate)  # before the push: a chunk whose norm fails can be given again
         self.counter.push(self.element(q, k, v, alpha, beta, u, w, self.chunk))
-        return o if self.norm is None else self.norm(o, gate)
+        return o
 
     def state(self):
         """The state after every chunk so far."""

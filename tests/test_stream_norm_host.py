@@ -31,3 +31,20 @@ def test_norm_sees_each_chunk_and_its_gate():
 def test_a_gate_without_a_norm_is_refused():
     with pytest.raises(ValueError):
         _stream(None).step(torch.zeros(1, 4, 1, 2), None, None, None, None, gate=torch.zeros(1, 4, 1, 2))
+
+
+def test_a_chunk_whose_norm_fails_is_not_in_the_stream():
+    """The caller corrects the gate and gives the chunk again: it counts once."""
+    def norm(o, gate):
+        if gate.shape != o.shape:
+            raise ValueError("gate")
+        return o * gate
+
+    s, plain = _stream(norm), _stream(None)
+    q = torch.full((1, 4, 1, 2), 3.0)
+    for i in range(3):
+        with pytest.raises(ValueError):
+            s.step(q, None, None, None, None, gate=q[:, :2])
+        y, o = s.step(q, None, None, None, None, gate=2 * torch.ones_like(q)), plain.step(q, None, None, None, None)
+        assert torch.equal(y, 2 * o) and s.counter.count == i + 1
+    assert torch.equal(s.state(), plain.state())
