@@ -11,11 +11,12 @@
 //           side by side, a few lanes hold them in registers, one pass over the data.
 //   tiles   any S: a first kernel reduces tiles of positions, a second one merges the tiles' results
 //           and applies them (its reads of a tensor up to L2's size hit L2).  A thread keeps the same
-//           channels (one vector) for all of its positions, so any D works at full vector width.  (One kernel
-//           whose CTAs keep a sample in the shared memory of a cluster was measured: 53 us against 27 on
-//           8 samples of 4096 x 320, which takes clusters of 16.)
-// Means and variances are merged pairwise from centred sums (count, mean, sum of squares about the
-// mean): a mean far above the deviation costs no digits.
+//           channels (one vector) for all of its positions.  (One kernel whose CTAs keep a sample in the shared
+//           memory of a cluster was measured: 53 us against 27 on 8 samples of 4096 x 320, which takes clusters of 16.)
+// Vectors are 16 bytes where the channels of a group (rows) or of a position (tiles) divide into them, one
+// channel where they do not.
+// Every result is (count, mean, sum of squares about the mean), and results are merged by their means' differences
+// from the first of them: a mean far above the deviation costs no digits beyond its own rounding.
 
 #include <algorithm>
 #include <type_traits>
@@ -532,6 +533,7 @@ struct PosStream {
         for (int k = 0; k + 1 < AHEAD; ++k) request(k, k);
     }
     __device__ __forceinline__ bool more() const { return s < end; }
+    __device__ __forceinline__ int positions() const { return s < end ? (end - s + RL - 1) / RL : 0; }
     // The current position's vectors; requests the one AHEAD - 1 further on.
     __device__ __forceinline__ void get(Pack<IO, V> (&x)[NT]) {
         if constexpr (RING) {
@@ -596,6 +598,11 @@ __device__ __forceinline__ void visit_pieces(const NormArgs &p, int n, int g, co
     }
 }
 
+// Positions that a thread sums up before it moves its mean.  (A mean moved by d / count at every position stops
+// moving once that is below half an ulp of it: 16384 positions of mean 1000 and deviation 0.5 were off by 60
+// half-ulps.  A mean in two parts, moved once a block, is off by one.  Blocks of 8: 1 to 2 % slower; of 32: 1 % faster.)
+constexpr int kStatBlock = 16;
+
 template <typename IO, int V>
 __global__ void __launch_bounds__(kTileThreads, 2) norm_tile_stats_kernel(NormArgs p) {
     __shared__ float sh_mean[kTileThreads * V], sh_m2[kTileThreads * V];
@@ -607,20 +614,53 @@ __global__ void __launch_bounds__(kTileThreads, 2) norm_tile_stats_kernel(NormAr
     in.t[0] = p.x;
     using U = Unit<V>;
     constexpr int NU = kUnits<V>;
-    U neg[NU], m2[NU];  // minus the mean, the sum of squares about it
+    // The mean so far is lo - neg, m2 the sum of squares about it, both of cnt positions.  A block's sums s of
+    // d = x + neg and q of d^2 move the mean by t - lo, t = (cnt lo + s) / (cnt + block), and add
+    // q + cnt lo^2 - (cnt + block) t^2 to m2.  It starts with the first position, so d has the size of the deviation.
+    U neg[NU], lo[NU], m2[NU];
 #pragma unroll
-    for (int u = 0; u < NU; ++u) neg[u] = m2[u] = both<U>(0.f);
+    for (int u = 0; u < NU; ++u) neg[u] = lo[u] = m2[u] = both<U>(0.f);
     float cnt = 0.f;
-    for (in.start(); in.more(); in.next()) {
+    in.start();
+    int left = in.positions();
+    if (left > 0) {
         Pack<IO, V> x[1];
         in.get(x);
-        cnt += 1.f;
-        const U f = both<U>(-__fdividef(1.f, cnt));
+        in.next();
+#pragma unroll
+        for (int u = 0; u < NU; ++u) neg[u] = mul(x[0].unit(u), both<U>(-1.f));
+        cnt = 1.f;
+        --left;
+    }
+    while (left > 0) {
+        // (a first block of 4: about a first value far from the others, sums of 16 would lose five bits to t)
+        const int block = min(left, cnt == 1.f ? kStatBlock / 4 : kStatBlock);
+        left -= block;
+        U s[NU], q[NU];
+#pragma unroll
+        for (int u = 0; u < NU; ++u) s[u] = q[u] = both<U>(0.f);
+#pragma unroll 4
+        for (int k = 0; k < block; ++k) {
+            Pack<IO, V> x[1];
+            in.get(x);
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+                const U d = add(x[0].unit(u), neg[u]);
+                s[u] = add(s[u], d);
+                q[u] = fma(d, d, q[u]);
+            }
+            in.next();
+        }
+        const U n_old = both<U>(cnt);
+        cnt += (float)block;
+        const U inv = both<U>(__fdividef(1.f, cnt)), minus = both<U>(-1.f);
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
-            const U xu = x[0].unit(u), d = add(xu, neg[u]);
-            neg[u] = fma(d, f, neg[u]);
-            m2[u] = fma(d, add(xu, neg[u]), m2[u]);
+            const U w = fma(n_old, lo[u], s[u]), t = mul(w, inv);
+            m2[u] = add(m2[u], fma(mul(w, minus), t, fma(mul(n_old, lo[u]), lo[u], q[u])));
+            const U at = fma(t, minus, neg[u]);                // minus the new mean, rounded,
+            lo[u] = add(t, fma(neg[u], minus, at));            // and what it lacks
+            neg[u] = at;
         }
     }
     const int width = t.c1 - t.c0, n = t.s1 - t.s0;
