@@ -1106,9 +1106,14 @@ prism_status prism_group_norm_fwd(const prism_norm_shape *shape, const void *x, 
     if (st != PRISM_OK) return st;
     const prism_norm_shape &s = *shape;
     const size_t n = (size_t)s.N * s.S * s.C * (s.io == PRISM_F32 ? 4 : 2), groups = (size_t)s.N * s.G * 4;
-    if (n == 0) return PRISM_OK;
-    if (!x || !y || !aligned16(x) || !aligned16(y) || !aligned16(gate)) return PRISM_ERR_INVALID_ARG;
     if (!aligned4(weight) || !aligned4(bias) || !aligned4(mean) || !aligned4(rstd)) return PRISM_ERR_INVALID_ARG;
+    if (n == 0) {  // statistics over no positions: NaN (every byte 255)
+        cudaError_t err = cudaSuccess;
+        if (mean && groups > 0) err = cudaMemsetAsync(mean, 255, groups, (cudaStream_t)stream);
+        if (rstd && groups > 0 && err == cudaSuccess) err = cudaMemsetAsync(rstd, 255, groups, (cudaStream_t)stream);
+        return cuda_status(err);
+    }
+    if (!x || !y || !aligned16(x) || !aligned16(y) || !aligned16(gate)) return PRISM_ERR_INVALID_ARG;
     const NormPlan pl = plan_of(s, false);
     const size_t need = stat_bytes(s, pl);
     if (need > 0 && (!workspace || ws_bytes < need || ((uintptr_t)workspace & 255u))) return PRISM_ERR_INVALID_ARG;

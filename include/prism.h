@@ -363,7 +363,7 @@ prism_status prism_group_norm_fwd_workspace_size(const prism_norm_shape *shape, 
  *                                   aligned; needs no clearing; may be NULL where the size is 0
  * x, gate and y dense and 16-byte aligned, the others 4-byte aligned; no output may overlap an
  * input or another output.  C <= 2^20, S <= 2^30, N <= 2^24, N*G < 2^31, N*S*C <= 2^40.  All
- * arithmetic in fp32, y rounded once.  With N or S of zero nothing is written.
+ * arithmetic in fp32, y rounded once.  With S of zero mean and rstd are NaN (statistics over nothing).
  */
 prism_status prism_group_norm_fwd(const prism_norm_shape *shape, const void *x, const float *weight,
                                   const float *bias, const void *gate, void *y, float *mean,
