@@ -535,13 +535,17 @@ def _new(like, shape) -> torch.Tensor:
     return torch.empty_like(like) if like.shape == shape and like.is_contiguous() else like.new_empty(shape)
 
 
-def _handed_out(stream, device, *tensors) -> None:
-    """Results made on another stream than the current one: the current one, where the caller is going to use
-    them, keeps their memory from being handed out again too early."""
+def _on_other_stream(stream, device, used, made) -> None:
+    """After a call on another stream than the current one: the memory of what it was given (`used`) is not handed out
+    again before that stream is through with it, so a caller may pass temporaries, and the memory of its results (`made`) not
+    before the current stream is, where the caller is going to use them."""
     if stream is not None:
         here = torch.cuda.current_stream(device)
         if stream != here:
-            for t in tensors:
+            for t in used:
+                if t is not None:
+                    t.record_stream(stream)
+            for t in made:
                 if t is not None:
                     t.record_stream(here)
 
@@ -637,7 +641,7 @@ def prism_decay_scan_fwd(q, k, v, decay, S0=None, lengths=None, *, o=None, S_fin
                _ptr(lengths), _ptr(o), _ptr(S_final), _ptr(ws), _size(ws), _stream(stream, dev))
     if rc != PRISM_OK:
         raise PrismError(rc, "prism_decay_scan_fwd")
-    _handed_out(stream, dev, o, S_final)
+    _on_other_stream(stream, dev, (q, k, v, decay, S0, lengths, o, S_final, ws), (o, S_final))
     return o, S_final
 
 
@@ -665,7 +669,7 @@ def prism_decay_scan_bwd(q, k, v, decay, S0=None, lengths=None, *, dO, dS_final=
                _ptr(out["dS0"]), _ptr(ws), _size(ws), _stream(stream, dev))
     if rc != PRISM_OK:
         raise PrismError(rc, "prism_decay_scan_bwd")
-    _handed_out(stream, dev, *out.values())
+    _on_other_stream(stream, dev, (q, k, v, decay, S0, lengths, dO, dS_final, ws), out.values())
     return out
 
 
@@ -686,7 +690,7 @@ def prism_decay_step(q, k, v, decay, S, *, o=None, stream=None):
                _ptr(o), _stream(stream, dev))
     if rc != PRISM_OK:
         raise PrismError(rc, "prism_decay_step")
-    _handed_out(stream, dev, o)
+    _on_other_stream(stream, dev, (q, k, v, decay, S, o), (o,))
     return o
 
 
@@ -735,7 +739,7 @@ def prism_group_norm_fwd(x, groups, weight=None, bias=None, gate=None, *, eps=1e
                _ptr(y), _ptr(mean), _ptr(rstd), _ptr(ws), _size(ws), _stream(stream, dev))
     if rc != PRISM_OK:
         raise PrismError(rc, "prism_group_norm_fwd")
-    _handed_out(stream, dev, y, mean, rstd)
+    _on_other_stream(stream, dev, (x, weight, bias, gate, y, ws), (y, mean, rstd))
     return y, mean, rstd
 
 
@@ -766,5 +770,5 @@ def prism_group_norm_bwd(x, groups, mean, rstd, weight=None, bias=None, gate=Non
                _ptr(out.get("dbias")), _ptr(ws), _size(ws), _stream(stream, dev))
     if rc != PRISM_OK:
         raise PrismError(rc, "prism_group_norm_bwd")
-    _handed_out(stream, dev, *out.values())
+    _on_other_stream(stream, dev, (x, mean, rstd, weight, bias, gate, dy, ws), out.values())
     return out
