@@ -29,14 +29,11 @@
 // Every wait is a bounded mbarrier poll that records PRISM_ERR_TIMEOUT in the library's producer
 // status word.
 
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <algorithm>
-#include <mutex>
 
 #include "chunk_common.cuh"
 #include "producer.cuh"
+#include "tensor_map.cuh"
 
 namespace prism {
 namespace {
@@ -484,24 +481,10 @@ __global__ void __launch_bounds__(RingLayout<D>::THREADS, 1)
     if (warp == LY::MMAW) tmem_dealloc(tb, 512);
 }
 
-// The driver's tensor-map encoder, fetched once through the runtime (no libcuda link).
-PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    });
-    return fn;
-}
-
 // 4-D map over bf16 weights [H, L, d, d] (row = output index): dims {d_in, d_out, L, H}, box
 // {64, d, 1, 1} (one 64-column block of one (h, l) matrix).
 bool weight_map(CUtensorMap *m, const void *base, int H, int L, int d, int rows) {
-    auto enc = map_encoder();
+    auto enc = tensor_map_encode_fn();
     if (!enc) return false;
     const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)d, (cuuint64_t)L, (cuuint64_t)H};
     const cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)d * d * 2, (cuuint64_t)L * d * d * 2};
@@ -514,7 +497,7 @@ bool weight_map(CUtensorMap *m, const void *base, int H, int L, int d, int rows)
 
 // x or v [B,T,H,d] bf16 as a 4-D map {d, H, T, B}; box {64, 1, rows, 1}, 128-byte swizzle.
 bool act_map(CUtensorMap *m, const void *base, int B, int T, int H, int d, int rows) {
-    auto enc = map_encoder();
+    auto enc = tensor_map_encode_fn();
     if (!enc) return false;
     const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
     const cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)H * d * 2, (cuuint64_t)T * H * d * 2};
@@ -528,7 +511,7 @@ bool act_map(CUtensorMap *m, const void *base, int B, int T, int H, int d, int r
 // u or w [B,T,H,L,d] bf16 as a 5-D map {d, L, H, T, B}; box {16, 1, 1, 32, 1} (one epilogue
 // warp's block of one rank), 32-byte swizzle.
 bool out_map(CUtensorMap *m, void *base, int B, int T, int H, int L, int d) {
-    auto enc = map_encoder();
+    auto enc = tensor_map_encode_fn();
     if (!enc) return false;
     const cuuint64_t dims[5] = {(cuuint64_t)d, (cuuint64_t)L, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
     const cuuint64_t strides[4] = {(cuuint64_t)d * 2, (cuuint64_t)L * d * 2, (cuuint64_t)H * L * d * 2,

@@ -30,12 +30,8 @@
 // by side along N, and two 64-row operands are stacked into one M = 128 instruction.  Every wait is
 // a bounded mbarrier poll that records PRISM_ERR_TIMEOUT when it runs out.
 
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include <mutex>
-
 #include "chunk_common.cuh"
+#include "tensor_map.cuh"
 
 namespace prism {
 namespace {
@@ -1699,24 +1695,9 @@ __global__ void __launch_bounds__(StateLayout<DK, RL, BV_>::THREADS, 1) gdn_stat
     if (warp == 0) tmem_dealloc(tb, LY::TCOLS);
 }
 
-// Host: the driver's tensor-map encoder, fetched once through the runtime (no libcuda link).
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    });
-    return fn;
-}
-
 // 4-D map over a bf16 activation [B, T, H, d]: dims {d, H, T, B}, box {box_d, 1, C, 1}.
 bool act_map(CUtensorMap *m, const void *base, int B, int T, int H, int d, int box_d) {
-    auto enc = tensor_map_encoder();
+    auto enc = tensor_map_encode_fn();
     if (!enc) return false;
     const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
     const cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)H * d * 2, (cuuint64_t)T * H * d * 2};
