@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(128) decay_carry_kernel(const __grid_constant_
 }
 
 template <typename IO>
-__global__ void decay_group_sum_kernel(DecayGroupSum a) {
+__global__ void decay_group_sum_kernel(const __grid_constant__ DecayGroupSum a) {
     dependent_wait();
     const int which = blockIdx.y, d = a.d[which], div = a.div;
     const float *part = a.part[which];
