@@ -50,19 +50,6 @@ __device__ __forceinline__ void st16(uint8_t *base, uint32_t off, uint4 v) {
     *reinterpret_cast<uint4 *>(base + off) = v;
 }
 
-template <int BV>
-__device__ __forceinline__ uint32_t vt_off(int row, int col) {
-    // x BV tile: 64B swizzle when BV = 32, 128B when BV = 64
-    if constexpr (BV == 32) return sw64_off(row, col);
-    else return sw128_off(row, col, 0);
-}
-
-template <int BV>
-__device__ __forceinline__ uint64_t desc_vt(uint32_t base, int ks) {
-    if constexpr (BV == 32) return desc_mn_sw64(base, ks);
-    else return desc_mn_sw128(base, ks, C * 128);  // a single MN block; LBO unused
-}
-
 // hi / lo bf16 pair of 8 floats
 __device__ __forceinline__ void split8(const float *x, uint4 &hi, uint4 &lo) {
     uint32_t h[4], l[4];
@@ -78,19 +65,6 @@ __device__ __forceinline__ void split8(const float *x, uint4 &hi, uint4 &lo) {
     lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-// A row of BV fp32 values as a hi / lo pair into two x BV tiles.
-template <int BV>
-__device__ __forceinline__ void store_row_split(uint8_t *hi, uint8_t *lo, int row, const float *x) {
-#pragma unroll
-    for (int c8 = 0; c8 < BV / 8; ++c8) {
-        uint4 h, l;
-        split8(x + c8 * 8, h, l);
-        const uint32_t off = vt_off<BV>(row, c8 * 8);
-        st16(hi, off, h);
-        st16(lo, off, l);
-    }
-}
-
 // 32 fp32 values at (row, col .. col+31) of K-major SW128 tiles, as a hi / lo pair or hi only.
 __device__ __forceinline__ void store32_split(uint8_t *hi, uint8_t *lo, int row, int col,
                                               const float *x, uint32_t block_bytes = 0) {
@@ -104,19 +78,6 @@ __device__ __forceinline__ void store32_split(uint8_t *hi, uint8_t *lo, int row,
     }
 }
 
-// BV consecutive TMEM columns of this thread's lane (warp-collective).
-template <int BV>
-__device__ __forceinline__ void ld_row(uint32_t tbase, int warp, uint32_t col, float *x) {
-#pragma unroll
-    for (int c = 0; c < BV; c += 32) {
-        float v[32];
-        tmem_ld32(taddr(tbase, 32 * warp, col + c), v);
-        tmem_wait_ld();
-#pragma unroll
-        for (int j = 0; j < 32; ++j) x[c + j] = v[j];
-    }
-}
-
 // Shared-memory writes become visible to the tensor core and earlier tcgen05.ld complete before
 // the issuing thread proceeds.
 __device__ __forceinline__ void sync_for_mma() {
@@ -124,19 +85,6 @@ __device__ __forceinline__ void sync_for_mma() {
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-}
-
-// D (+)= (A_hi + A_lo)(B_hi + B_lo) without the lo*lo term; K = 16 * nks.  Pass alo / blo = 0 to
-// skip a split.  `acc` says whether the first product accumulates onto D.
-template <class FA, class FB>
-__device__ __forceinline__ void mma_split(uint32_t d, uint32_t idesc, int nks, FA adesc, FB bdesc,
-                                          uint32_t ahi, uint32_t alo, uint32_t bhi, uint32_t blo,
-                                          bool acc) {
-    for (int ks = 0; ks < nks; ++ks) mma_bf16(d, adesc(ahi, ks), bdesc(bhi, ks), idesc, acc || ks > 0);
-    if (blo)
-        for (int ks = 0; ks < nks; ++ks) mma_bf16(d, adesc(ahi, ks), bdesc(blo, ks), idesc, 1);
-    if (alo)
-        for (int ks = 0; ks < nks; ++ks) mma_bf16(d, adesc(alo, ks), bdesc(bhi, ks), idesc, 1);
 }
 
 // Two fp32 lanes per instruction (the packed f32x2 arithmetic of sm_100): d = a * b + c, each

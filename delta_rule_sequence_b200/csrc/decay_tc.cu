@@ -195,6 +195,7 @@ struct SumLayout {
     static constexpr uint32_t BYTES = YP + NYB * YP_BYTES + 1024;
     static constexpr uint32_t cY = 0, cD = 384;          // TMEM columns: the weighted Y, the product
     static_assert(BYTES + 2048 <= 227 * 1024, "shared memory budget");
+    static_assert(cY + 192 * NYB <= cD && cD + D2 <= 512, "TMEM columns");
 };
 
 template <int D1, int D2>

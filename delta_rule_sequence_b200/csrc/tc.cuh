@@ -48,25 +48,11 @@ __device__ __forceinline__ uint64_t make_desc(uint32_t saddr, uint32_t lbo_bytes
     return d;
 }
 
-// K-major SW128 operand (rows = M or N, contiguous K), k-step `ks` of 16 elements.
-__device__ __forceinline__ uint64_t desc_k_sw128(uint32_t base, int ks, uint32_t block_bytes) {
-    const int k = ks * 16;
-    return make_desc(base + (k >> 6) * block_bytes + (k & 63) * 2, 16, 1024, 2);
-}
-
-// MN-major SW128 operand stored [k][mn] (contiguous MN, 64-element blocks `block_bytes` apart),
-// k-step `ks` of 16 rows.
-__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t base, int ks, uint32_t block_bytes) {
-    return make_desc(base + ks * 16 * 128, block_bytes, 1024, 2);
-}
-
-// MN-major SW64 operand stored [k][mn] with 32 MN elements per row, k-step `ks` of 16 rows.
-__device__ __forceinline__ uint64_t desc_mn_sw64(uint32_t base, int ks) {
-    return make_desc(base + ks * 16 * 64, 0, 512, 4);
-}
-
 // k-step offsets of an operand, in the descriptor's 16-byte address units (added to a base
-// descriptor: the start-address field cannot carry because shared addresses stay below 256 KB).
+// descriptor: the start-address field cannot carry because shared addresses stay below 256 KB).  Steps are of
+// 16; base descriptors: K-major SW128 (rows = M or N, contiguous K) make_desc(p, 16, 1024, 2), MN-major SW128
+// (stored [k][mn], 64-element blocks block_bytes apart) make_desc(p, block_bytes, 1024, 2), MN-major SW64 (32 MN
+// elements a row) make_desc(p, 0, 512, 4).
 __host__ __device__ constexpr uint32_t koff_k_sw128(int ks, uint32_t block_bytes) {
     return (((uint32_t)(ks * 16) >> 6) * block_bytes + (uint32_t)((ks * 16) & 63) * 2) >> 4;
 }
@@ -175,16 +161,6 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_
 // ------------------------------------------------------------------------------------------------
 // tcgen05
 
-__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                         uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n"
-        :
-        : "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
-}
-
 // Arrive once on `bar` when every tcgen05 operation this thread issued so far has completed.
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
@@ -272,15 +248,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
                  ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-          "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-          "r"(r[15])
-        : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
     asm volatile(
@@ -398,20 +365,6 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
 // Barrier among `nthreads` threads (whole warps) on hardware barrier `id` (0 is __syncthreads).
 __device__ __forceinline__ void named_sync(uint32_t id, uint32_t nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
-}
-
-// Barrier among `nthreads` threads that also ORs a predicate across them (uniform result).
-__device__ __forceinline__ bool named_sync_or(uint32_t id, uint32_t nthreads, bool pred) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, %2, %3, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}\n"
-        : "=r"(r)
-        : "r"((uint32_t)pred), "r"(id), "r"(nthreads)
-        : "memory");
-    return r != 0;
 }
 
 // Wait for phase `parity` of `bar` to complete.  Gives up after `limit` polls (each poll blocks
