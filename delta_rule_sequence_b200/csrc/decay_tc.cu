@@ -178,15 +178,18 @@ __device__ __forceinline__ void zero_rows(uint8_t *tile, int n, int tid, int nth
 
 template <int D1, int D2>
 struct SumLayout {
-    // Warps that weigh Y, that hold the state.  (8 for Y: 2 % slower on 16 heads of 65536 tokens of 128, 3 % on a padded
-    // batch of 64-wide heads.)
-    static constexpr int YW = 16, SW = 8;
+    // Warps that weigh Y, that hold the state.  At 64 x 128 there is one buffer of the weighted Y, and twice the warps
+    // do not work ahead of the products.  (16 heads of 65536 tokens, 16 warps against 8: 128 x 128 338 us against 345,
+    // 128 x 64 and 64 x 64 the same, 64 x 128 289 against 284; its padded batch of 32 x 4 275 against 272.)
+    static constexpr int YW = D1 == 64 && D2 == 128 ? 8 : 16, SW = 8;
     static constexpr int LOADW = YW + SW, MMAW = LOADW + 1;
-    static constexpr int THREADS = 32 * (LOADW + 4);     // whole warpgroups: two warps of the last have no role
-    // Registers of a thread by role, as in the pass (launched with 72).
+    // With 16, registers are shared out by role as in the pass (launched with 72), by whole warpgroups: two warps of
+    // the last have no role.  With 8 each thread has 96 throughout.
+    static constexpr bool SHARED_OUT = YW == 16;
+    static constexpr int THREADS = 32 * (SHARED_OUT ? LOADW + 4 : MMAW + 1);
     static constexpr int RS = 112, RY = 56, RM = 40;
-    static constexpr int SHARES = (SW * RS + YW * RY + 4 * RM) * 32;
-    static_assert(THREADS == 896 && SHARES <= 72 * THREADS, "register shares");
+    static constexpr int SHARES = SHARED_OUT ? (SW * RS + YW * RY + 4 * RM) * 32 : 0;
+    static_assert(!SHARED_OUT || (THREADS == 896 && SHARES <= 72 * THREADS), "register shares");
     // The weighted Y: two buffers of three terms in TMEM, or (D1 = 64) one or two in shared memory.
     static constexpr int NYB = D1 == 64 && D2 == 128 ? 1 : 2;
     static constexpr int NST = 3;
@@ -253,7 +256,8 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
             w_last[j] = wk.reverse ? pw.w[j] : pw.at(max(wk.n(wk.nch - 1) - 1 - j, 0));
     __syncthreads();
 
-    if (warp >= LY::LOADW) setmaxnreg_dec<LY::RM>();
+    if constexpr (LY::SHARED_OUT)
+        if (warp >= LY::LOADW) setmaxnreg_dec<LY::RM>();
     if (warp == LY::LOADW) {
         if (lane == 0 && !p.stall) {
             int i = min(NST, wk.nch);
@@ -299,7 +303,7 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
     } else if (warp > LY::MMAW) {
         // (no role)
     } else if (warp < LY::YW) {
-        setmaxnreg_dec<LY::RY>();
+        if constexpr (LY::SHARED_OUT) setmaxnreg_dec<LY::RY>();
         const int q = warp & 3, j1 = CT / (LY::YW / 4) * (warp >> 2), m = 32 * q + lane;
         for (int i = 0; i < wk.nch; ++i) {
             const int st = i % NST, pb = i % LY::NYB, n = wk.n(i);
@@ -327,7 +331,7 @@ __global__ void __launch_bounds__(SumLayout<D1, D2>::THREADS, 1)
             }
         }
     } else {
-        setmaxnreg_inc<LY::RS>();
+        if constexpr (LY::SHARED_OUT) setmaxnreg_inc<LY::RS>();
         const int sw = warp - LY::YW, q = sw & 3, half = sw >> 2, m = product_row<D1>(q, lane);
         constexpr int NC = D2 / 2;
         float r[NC];
