@@ -151,11 +151,16 @@ def _ptr(x):
     return None if x is None else x.data_ptr()
 
 
+# The current stream's handle: torch.cuda.current_stream without its object (1 us a call), where this torch has that.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _stream(stream, device):
     """The stream to launch on: the caller's (which must belong to `device`), else the current
     stream of `device` (not of whichever device happens to be current)."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)  # current_stream(device) without its object
+        return _current_raw_stream(device.index)
     if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
     return stream.cuda_stream

@@ -1,4 +1,6 @@
 """prism_query_device_status takes a device in any spelling that torch.device takes."""
+import importlib.util
+
 import pytest
 import torch
 
@@ -18,7 +20,7 @@ def library(monkeypatch):
     lib = _Library()
     monkeypatch.setattr(P, "load_library", lambda: lib)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 1000 + int(index.__index__()))
+    monkeypatch.setattr(P, "_current_raw_stream", lambda index: 1000 + int(index.__index__()))
     return lib
 
 
@@ -43,6 +45,16 @@ def test_other_devices_are_refused(library):
     with pytest.raises(ValueError):
         P.prism_query_device_status(None, device="cpu")
     assert not hasattr(library, "asked")
+
+
+def test_a_torch_without_the_raw_stream_lookup(monkeypatch):
+    """The lookup is not part of torch's public interface: without it the stream's object gives the handle."""
+    source = importlib.util.find_spec(P.__name__)
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    module = importlib.util.module_from_spec(source)
+    source.loader.exec_module(module)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda index: type("Stream", (), {"cuda_stream": 2000 + index}))
+    assert module._stream(None, torch.device("cuda", 3)) == 2003
 
 
 @pytest.mark.gpu
