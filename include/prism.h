@@ -284,9 +284,11 @@ prism_status prism_decay_scan_fwd_workspace_size(const prism_decay_shape *shape,
  * No other overlap of an output with an input or output is allowed.  B, H <= 65535, B*H <= 2^24,
  * T <= 2^26.
  * States and sums are fp32.  bf16 outputs are rounded to nearest even; inside, the products of a
- * chunk and the state are rounded to bf16 once where they enter an output's product, never where
- * they enter a state.  A non-finite value in a valid token reaches outputs of its whole 128-token
- * chunk and of every later token.  Results do not depend on the run (no atomics).
+ * chunk and the state are rounded to bf16 once where they enter an output's product, so outputs
+ * are off by up to two roundings where one would do.  What enters S_final keeps 24 bits; what enters
+ * the running state that outputs are read from keeps 16.  A non-finite value in a valid token reaches
+ * outputs of its whole chunk (128 tokens, 64 at fp32) and of every later token.  Results do not
+ * depend on the run (no atomics).
  */
 prism_status prism_decay_scan_fwd(const prism_decay_shape *shape, const void *q, const void *k,
                                   const void *v, const float *decay, const float *S0,
@@ -294,8 +296,9 @@ prism_status prism_decay_scan_fwd(const prism_decay_shape *shape, const void *q,
                                   size_t ws_bytes, void *stream);
 
 /* prism_decay_scan_bwd_workspace_size -- bytes of device workspace prism_decay_scan_bwd needs for
- * `shape` (the segments' states and state gradients; with Hkv < H also fp32 gradients of one shared
- * operand per query head).  Depends on the current device's SM count.  Writes *bytes. */
+ * `shape` (the segments' states and state gradients; with Hkv < H also fp32 gradients of k and of v
+ * for every query head, 4 B T H (dk + dv) bytes).  Depends on the current device's SM count.  Writes
+ * *bytes. */
 prism_status prism_decay_scan_bwd_workspace_size(const prism_decay_shape *shape, size_t *bytes);
 
 /*
